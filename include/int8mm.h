@@ -350,6 +350,111 @@ int int8_gemm_i32(const int8_t *X_i8, int64_t M, int64_t K, const int8_t *W_i8,
 int int8mm_kernel_config(int64_t M, int64_t N, int64_t K, int32_t *cfg);
 
 /*
+ * ---- Block-scaled 8-bit floating point -------------------------------
+ *
+ * The other 8-bit form of a linear layer: e4m3 numbers (4 exponent bits, 3
+ * mantissa bits, no infinities, largest 448) with one fp32 scale per block
+ * of 128, for activations per token, for weights per 128 features.  An
+ * outlier column costs precision only within its own block, so nothing is
+ * detected and no fp16 path is needed.  Serving operators: quantizers for
+ * the three places a layer's input comes from, and the product.
+ *
+ * Conventions beyond the shared ones above
+ *   - A 16-bit tensor is fp16 or bf16 (int8mm_type); all 16-bit tensors of a
+ *     call have one type.
+ *   - KB = ceil(K / 128).  K may end inside a block: its scale is that of
+ *     the columns there are.
+ *   - Quantization of a block with absmax a = max(max |x|, 2^-100):
+ *     scale = RN32(a / 448), q = e4m3_rne(RN32(x * RN32(448 / a))), x ~ q * scale.
+ *     fp8_quantize is therefore reproducible bit for bit.
+ *   - Inputs need not be finite: a NaN or an infinity leaves as NaN (an
+ *     infinity also makes its block's scale infinite), and the products
+ *     that meet it are NaN.
+ *   - Everything runs in one launch (or several in a row for more than 2^20
+ *     rows) on `stream`, without a workspace; results do not depend on
+ *     timing, and calls on different streams may overlap.
+ */
+typedef enum { INT8MM_F16 = 0, INT8MM_BF16 = 1 } int8mm_type;
+
+/*
+ * Packed e4m3 weight W_f8 (N x K, indexed along K): 2 KB blocks of 16
+ * features x 128 columns, K zero-padded to a multiple of 128:
+ *     byte offset of (n, k) = ((n/16) * KB + k/128) * 2048
+ *                             + (((k/16) % 8) * 16 + n % 16) * 16 + k % 16.
+ * A half block is one 64-lane x 16-byte load, a block one matrix operand.
+ * Bytes of a packed N x K weight; -1 if out of range or misaligned
+ * (K % 16, N % 16).
+ */
+int64_t fp8_packed_size(int64_t N, int64_t K);
+
+/*
+ * fp8_quantize_weight -- once, at load: W [K][N] (16-bit, row-major) -> W_f8
+ * (packed) and w_scale [ceil(N/128)][KB], one scale per 128 x 128 block.
+ * K % 16 == 0, N % 16 == 0, N * roundup(K, 128) <= INT8MM_MAX_MN, pointers
+ * 16-byte aligned.
+ */
+int fp8_quantize_weight(const void *W, int type, int64_t K, int64_t N,
+                        void *W_f8, float *w_scale, hipStream_t stream);
+
+/* Packs e4m3 weights that are already quantized: src [N][K] row-major (a
+ * checkpoint's bytes; its scales [ceil(N/128)][KB] are used as they are). */
+int fp8_pack_weight(const void *src, int64_t N, int64_t K, void *W_f8,
+                    hipStream_t stream);
+
+/*
+ * fp8_quantize -- X [M][K] (16-bit) -> X_f8 [M][K] e4m3, row-major, and
+ * x_scale [KB][M]: the scales of one block of columns for all tokens are
+ * contiguous, as the product reads them.  K % 16 == 0, M * K <=
+ * INT8MM_MAX_MN, pointers 16-byte aligned.  M == 0 or K == 0 is a no-op.
+ */
+int fp8_quantize(const void *X, int type, int64_t M, int64_t K, void *X_f8,
+                 float *x_scale, hipStream_t stream);
+
+/*
+ * fp8_rms_norm -- the root-mean-square norm before a linear layer, with the
+ * residual's addition in front and the quantizer behind it:
+ *     h = RN16(x + residual)                (h = x without a residual)
+ *     y = h / sqrt(mean(h^2) + eps) * weight           (fp32, not rounded)
+ *     X_f8, x_scale = fp8_quantize(y)
+ *   X, residual  in  [M][K]; residual may be NULL.
+ *   weight       in  [K], of the same 16-bit type.
+ *   eps          in  > 0, finite.
+ *   H            out [M][K], the new residual h; NULL if and only if
+ *                    residual is.  May be the residual's or X's own buffer.
+ * Sums are held in fp32.
+ */
+int fp8_rms_norm(const void *X, const void *residual, const void *weight,
+                 int type, int64_t M, int64_t K, float eps, void *H,
+                 void *X_f8, float *x_scale, hipStream_t stream);
+
+/*
+ * fp8_silu_mul -- the gated activation before a feed-forward's second
+ * product: gate_up [M][2K] (16-bit; a row is its K gates, then its K ups) ->
+ * the quantized g / (1 + exp(-g)) * u, in fp32 up to the quantizer.
+ * M * 2K <= INT8MM_MAX_MN.
+ */
+int fp8_silu_mul(const void *gate_up, int type, int64_t M, int64_t K,
+                 void *A_f8, float *a_scale, hipStream_t stream);
+
+/*
+ * fp8_matmul -- Y[m][n] = sum_b x_scale[b][m] * w_scale[n/128][b] *
+ * (sum over the columns k of block b of X_f8[m][k] * W_f8[n][k])  (+ bias[n]),
+ * accumulated in fp32 and rounded once to the 16-bit `type` of Y and bias.
+ * (Within 8 consecutive columns the matrix instruction keeps the bits of each
+ * exact product down to 2^-13 of the largest.)
+ *   X_f8, x_scale  in  as the quantizers above leave them.
+ *   W_f8, w_scale  in  as fp8_quantize_weight leaves them.
+ *   bias           in  [N] or NULL.
+ *   Y              out [M][N], row-major.
+ * K % 16 == 0, N % 16 == 0, M * K, M * N and N * roundup(K, 128) <=
+ * INT8MM_MAX_MN, pointers 16-byte aligned.  M == 0 or N == 0 is a no-op;
+ * K == 0 writes Y = bias (0 without one).
+ */
+int fp8_matmul(const void *X_f8, const float *x_scale, int64_t M, int64_t K,
+               const void *W_f8, const float *w_scale, int64_t N,
+               const void *bias, int type, void *Y, hipStream_t stream);
+
+/*
  * Profiling aid (not thread-safe; for benchmarks).  While enabled, every
  * int8_mixed_matmul call has the dispatch of its main kernel (the tiled
  * int8 GEMM, or the decode kernel for M <= 32) record a pair of HIP events

@@ -25,6 +25,8 @@ __all__ = [
     "timing_enable", "timing_read", "default_n_cap", "kpad", "rpad", "packed_size", "pack_rows",
     "kernel_config", "outlier_cache_size", "build_outlier_cache", "mixed_matmul_cached",
     "STATUS_OK", "STATUS_EINVAL", "STATUS_EALIGN", "STATUS_EWORKSPACE", "STATUS_EHIP",
+    "FP8_BLOCK", "fp8_kpad", "fp8_pack_weight", "fp8_quantize_weight", "fp8_quantize",
+    "fp8_rms_norm", "fp8_silu_mul", "fp8_matmul",
     "STATUS_ESCRATCH", "FLAG_OVERFLOW", "FLAG_CACHE_MISS", "FLAG_CACHE_MISMATCH",
 ]
 
@@ -96,6 +98,21 @@ def load() -> ctypes.CDLL:
                                               ctypes.c_float, _vp, _vp, _i64, _vp]
     lib.int8mm_kernel_config.restype = ctypes.c_int
     lib.int8mm_kernel_config.argtypes = [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_int32)]
+    _i32 = ctypes.c_int
+    lib.fp8_packed_size.restype = ctypes.c_int64
+    lib.fp8_packed_size.argtypes = [_i64, _i64]
+    lib.fp8_quantize_weight.restype = ctypes.c_int
+    lib.fp8_quantize_weight.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _vp]
+    lib.fp8_pack_weight.restype = ctypes.c_int
+    lib.fp8_pack_weight.argtypes = [_vp, _i64, _i64, _vp, _vp]
+    lib.fp8_quantize.restype = ctypes.c_int
+    lib.fp8_quantize.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _vp]
+    lib.fp8_rms_norm.restype = ctypes.c_int
+    lib.fp8_rms_norm.argtypes = [_vp, _vp, _vp, _i32, _i64, _i64, ctypes.c_float, _vp, _vp, _vp, _vp]
+    lib.fp8_silu_mul.restype = ctypes.c_int
+    lib.fp8_silu_mul.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _vp]
+    lib.fp8_matmul.restype = ctypes.c_int
+    lib.fp8_matmul.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _vp]
     _lib = lib
     return lib
 
@@ -480,3 +497,7 @@ def timing_read():
     n = ctypes.c_int64(0)
     _check(load().int8mm_timing_read(ctypes.byref(ms), ctypes.byref(n)))
     return ms.value, n.value
+
+
+from .fp8 import (FP8_BLOCK, fp8_kpad, fp8_matmul, fp8_pack_weight, fp8_quantize,  # noqa: E402
+                  fp8_quantize_weight, fp8_rms_norm, fp8_silu_mul)

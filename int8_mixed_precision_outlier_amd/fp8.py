@@ -1,0 +1,188 @@
+"""The block-scaled 8-bit floating-point operators: e4m3 numbers with one fp32
+scale per block of 128 columns (include/int8mm.h, "Block-scaled 8-bit floating
+point").
+
+    W_f8, w_scale = fp8_quantize_weight(W)                  # once, offline
+    X_f8, x_scale, H = fp8_rms_norm(X, g, residual=R)       # or fp8_quantize(X)
+    GU = fp8_matmul(X_f8, x_scale, W_f8, w_scale)
+    A_f8, a_scale = fp8_silu_mul(GU)
+
+Activations and weights are fp16 or bf16; e4m3 tensors are
+torch.float8_e4m3fn.  Serving operators: their results carry no gradient.
+Each call runs on the device of its first tensor, on that device's current
+stream unless `stream` is given; buffers a call allocates are allocated on
+its stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import _check, _ptr, load
+
+__all__ = ["FP8_BLOCK", "fp8_kpad", "fp8_pack_weight", "fp8_quantize_weight", "fp8_quantize",
+           "fp8_rms_norm", "fp8_silu_mul", "fp8_matmul"]
+
+FP8_BLOCK = 128
+_E4M3 = torch.float8_e4m3fn
+_TYPES = {torch.float16: 0, torch.bfloat16: 1}  # int8mm_type
+
+
+def fp8_kpad(K: int) -> int:
+    """K rounded up to the 128-column blocks of the packed e4m3 layout."""
+    return (K + 127) // 128 * 128
+
+
+def _blocks(n: int) -> int:
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _tensor(t, name: str, dtypes, shape, device=None):
+    """A contiguous GPU tensor of one of `dtypes` and of `shape` (None: any
+    size), on `device` if given."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        want = tuple("any" if w is None else w for w in shape)
+        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call on {device}")
+    return t
+
+
+@contextlib.contextmanager
+def _launch(device, stream):
+    """Makes `device` (and `stream`, if given) current; yields the stream handle."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        else:
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _quantized(out, M, K, device):
+    """The (e4m3 [M, K], scales [ceil(K/128), M]) a quantizer writes: `out`, or new."""
+    if out is None:
+        return (torch.empty((M, K), dtype=_E4M3, device=device),
+                torch.empty((_blocks(K), M), dtype=torch.float32, device=device))
+    q, s = out
+    return (_tensor(q, "out[0]", (_E4M3,), (M, K), device),
+            _tensor(s, "out[1]", (torch.float32,), (_blocks(K), M), device))
+
+
+def fp8_pack_weight(Wq: torch.Tensor, stream=None) -> torch.Tensor:
+    """e4m3 weights [N,K] row-major (a checkpoint's, with scales [ceil(N/128),
+    ceil(K/128)]) -> the packed layout, as an e4m3 tensor [N, fp8_kpad(K)] (an
+    opaque buffer)."""
+    _tensor(Wq, "Wq", (_E4M3,), (None, None))
+    N, K = Wq.shape
+    with _launch(Wq.device, stream) as st:
+        out = torch.empty((N, fp8_kpad(K)), dtype=_E4M3, device=Wq.device)
+        _check(load().fp8_pack_weight(_ptr(Wq), N, K, _ptr(out), st))
+    return out
+
+
+def fp8_quantize_weight(W: torch.Tensor, stream=None):
+    """W fp16 or bf16 [K,N] -> (W_f8 packed e4m3 [N, fp8_kpad(K)], w_scale fp32
+    [ceil(N/128), ceil(K/128)]), one scale per 128 x 128 block."""
+    _tensor(W, "W", tuple(_TYPES), (None, None))
+    K, N = W.shape
+    with _launch(W.device, stream) as st:
+        W_f8 = torch.empty((N, fp8_kpad(K)), dtype=_E4M3, device=W.device)
+        w_scale = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
+        _check(load().fp8_quantize_weight(_ptr(W), _TYPES[W.dtype], K, N, _ptr(W_f8),
+                                          _ptr(w_scale), st))
+    return W_f8, w_scale
+
+
+def fp8_quantize(X: torch.Tensor, out=None, stream=None):
+    """X fp16 or bf16 [M,K] -> (X_f8 e4m3 [M,K], x_scale fp32 [ceil(K/128), M]).
+    `out`: such a pair to write into."""
+    _tensor(X, "X", tuple(_TYPES), (None, None))
+    M, K = X.shape
+    with _launch(X.device, stream) as st:
+        X_f8, x_scale = _quantized(out, M, K, X.device)
+        _check(load().fp8_quantize(_ptr(X), _TYPES[X.dtype], M, K, _ptr(X_f8), _ptr(x_scale), st))
+    return X_f8, x_scale
+
+
+def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 residual: torch.Tensor | None = None,
+                 residual_out: torch.Tensor | None = None, out=None, stream=None):
+    """The quantized root-mean-square norm of X [M,K] with weight [K]:
+    (X_f8, x_scale), or with `residual` [M,K], whose sum with X (rounded to
+    their type) is normed instead, (X_f8, x_scale, H) with H that sum.
+    `residual_out` takes H; it may be `residual` itself."""
+    _tensor(X, "X", tuple(_TYPES), (None, None))
+    M, K = X.shape
+    _tensor(weight, "weight", (X.dtype,), (K,), X.device)
+    if residual is not None:
+        _tensor(residual, "residual", (X.dtype,), (M, K), X.device)
+        if residual_out is not None:
+            _tensor(residual_out, "residual_out", (X.dtype,), (M, K), X.device)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    with _launch(X.device, stream) as st:
+        X_f8, x_scale = _quantized(out, M, K, X.device)
+        H = residual_out
+        if residual is not None and H is None:
+            H = torch.empty((M, K), dtype=X.dtype, device=X.device)
+        _check(load().fp8_rms_norm(_ptr(X), _ptr(residual), _ptr(weight), _TYPES[X.dtype], M, K,
+                                   ctypes.c_float(float(eps)), _ptr(H), _ptr(X_f8), _ptr(x_scale),
+                                   st))
+    return (X_f8, x_scale) if residual is None else (X_f8, x_scale, H)
+
+
+def fp8_silu_mul(gate_up: torch.Tensor, out=None, stream=None):
+    """gate_up fp16 or bf16 [M,2K] (K gates, then K ups) -> the quantized
+    silu(gate) * up: (A_f8 e4m3 [M,K], a_scale fp32 [ceil(K/128), M])."""
+    _tensor(gate_up, "gate_up", tuple(_TYPES), (None, None))
+    M, K2 = gate_up.shape
+    if K2 % 2:
+        raise ValueError(f"gate_up must have an even number of columns, got {K2}")
+    K = K2 // 2
+    with _launch(gate_up.device, stream) as st:
+        A_f8, a_scale = _quantized(out, M, K, gate_up.device)
+        _check(load().fp8_silu_mul(_ptr(gate_up), _TYPES[gate_up.dtype], M, K, _ptr(A_f8),
+                                   _ptr(a_scale), st))
+    return A_f8, a_scale
+
+
+def fp8_matmul(X_f8: torch.Tensor, x_scale: torch.Tensor, W_f8: torch.Tensor,
+               w_scale: torch.Tensor, bias: torch.Tensor | None = None,
+               out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Y [M,N] = the block-scaled product of X_f8 [M,K] (with x_scale
+    [ceil(K/128), M]) and the packed W_f8 [N, fp8_kpad(K)] (with w_scale
+    [ceil(N/128), ceil(K/128)]), plus `bias` [N].  Y and bias are of
+    `out_dtype` (fp16 or bf16; by default that of `out`, else of bias, else bf16)."""
+    _tensor(X_f8, "X_f8", (_E4M3,), (None, None))
+    M, K = X_f8.shape
+    dev = X_f8.device
+    _tensor(x_scale, "x_scale", (torch.float32,), (_blocks(K), M), dev)
+    _tensor(W_f8, "W_f8", (_E4M3,), (None, fp8_kpad(K)), dev)
+    N = W_f8.shape[0]
+    _tensor(w_scale, "w_scale", (torch.float32,), (_blocks(N), _blocks(K)), dev)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else bias.dtype if bias is not None else torch.bfloat16
+    if out_dtype not in _TYPES:
+        raise TypeError(f"out_dtype must be {' or '.join(map(str, _TYPES))}, got {out_dtype}")
+    if bias is not None:
+        _tensor(bias, "bias", (out_dtype,), (N,), dev)
+    if out is not None:
+        _tensor(out, "out", (out_dtype,), (M, N), dev)
+    with _launch(dev, stream) as st:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        _check(load().fp8_matmul(_ptr(X_f8), _ptr(x_scale), M, K, _ptr(W_f8), _ptr(w_scale), N,
+                                 _ptr(bias), _TYPES[out_dtype], _ptr(out), st))
+    return out

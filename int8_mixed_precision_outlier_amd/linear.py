@@ -1,5 +1,6 @@
-"""A torch module over the C-ABI: an fp16 linear layer whose forward pass is
-the LLM.int8() decomposed matmul.
+"""Torch modules over the C-ABI: an fp16 linear layer whose forward pass is
+the LLM.int8() decomposed matmul, and its block-scaled e4m3 counterpart with
+the norm that feeds it.
 
 The layer of the brain.gartu.xyz page's practical example ("Exemple
 pratique") replaces an nn.Linear (with bias) by an int8 layer with
@@ -11,8 +12,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (build_outlier_cache, mixed_matmul, mixed_matmul_cached, quantize_weight,
-               workspace_size)
+from . import (build_outlier_cache, fp8_matmul, fp8_pack_weight, fp8_quantize,
+               fp8_quantize_weight, fp8_rms_norm, mixed_matmul, mixed_matmul_cached,
+               quantize_weight, workspace_size)
 
 
 class Int8MixedLinear(torch.nn.Module):
@@ -83,4 +85,93 @@ class Int8MixedLinear(torch.nn.Module):
         return y.reshape(*x.shape[:-1], self.out_features)
 
 
-__all__ = ["Int8MixedLinear"]
+class Fp8RMSNorm(torch.nn.Module):
+    """The root-mean-square norm in front of Fp8BlockLinear layers, with the
+    residual's addition: forward(x, residual) gives ((e4m3, scales), h) with
+    h = x + residual, forward(x) the pair (e4m3, scales) alone.  x [..., K] of
+    the weight's type; the pair is 2-D, one row per token, and every
+    Fp8BlockLinear that reads this norm takes it as it is.
+    """
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6):
+        super().__init__()
+        if weight.dim() != 1 or weight.device.type != "cuda":
+            raise TypeError("weight must be a 1-D CUDA tensor")
+        self.register_buffer("weight", weight.detach().clone())
+        self.eps = float(eps)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        K = self.weight.numel()
+        if x.shape[-1] != K:
+            raise ValueError(f"expected last dimension {K}, got {x.shape[-1]}")
+        x2 = x.reshape(-1, K).contiguous()
+        if residual is None:
+            return fp8_rms_norm(x2, self.weight, eps=self.eps)
+        if residual.shape != x.shape:
+            raise ValueError(f"residual {tuple(residual.shape)}, x {tuple(x.shape)}")
+        q, s, h = fp8_rms_norm(x2, self.weight, eps=self.eps,
+                               residual=residual.reshape(-1, K).contiguous())
+        return (q, s), h.reshape(x.shape)
+
+
+class Fp8BlockLinear(torch.nn.Module):
+    """y = x . W^T + b with block-scaled e4m3 weights (quantized once, when the
+    module is built) and activations (quantized per call).
+
+    x: fp16 or bf16 [..., in_features], or the pair (e4m3 [M, in_features],
+    scales) that Fp8RMSNorm, fp8_quantize or fp8_silu_mul leaves; then y is
+    [M, out_features].  y is of the module's 16-bit type, the weight's at
+    first.  Buffers: w_f8 (packed), w_scale, bias or None.  For serving: y
+    carries no gradient.
+    """
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None):
+        super().__init__()
+        if weight.dim() != 2 or weight.device.type != "cuda":
+            raise TypeError("weight must be a 2-D CUDA tensor [out_features, in_features]")
+        if weight.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"weight must be fp16 or bf16, got {weight.dtype}")
+        w_f8, w_scale = fp8_quantize_weight(weight.detach().t().contiguous())
+        self._set(w_f8, w_scale, weight.shape[1], weight.dtype, bias)
+
+    def _set(self, w_f8, w_scale, in_features, dtype, bias):
+        self.register_buffer("w_f8", w_f8)
+        self.register_buffer("w_scale", w_scale)
+        if bias is not None:
+            bias = bias.detach().to(device=w_f8.device, dtype=dtype).contiguous()
+        self.register_buffer("bias", bias)
+        self.in_features, self.out_features = in_features, w_f8.shape[0]
+        self.dtype = dtype
+
+    @classmethod
+    def from_linear(cls, linear: torch.nn.Linear) -> "Fp8BlockLinear":
+        return cls(linear.weight, linear.bias)
+
+    @classmethod
+    def from_quantized(cls, weight: torch.Tensor, w_scale: torch.Tensor,
+                       bias: torch.Tensor | None = None,
+                       dtype: torch.dtype = torch.bfloat16) -> "Fp8BlockLinear":
+        """A checkpoint's e4m3 weight [out, in] with its scales
+        [ceil(out/128), ceil(in/128)]."""
+        self = cls.__new__(cls)
+        torch.nn.Module.__init__(self)
+        self._set(fp8_pack_weight(weight), w_scale.to(torch.float32).contiguous(), weight.shape[1],
+                  dtype, bias)
+        return self
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"bias={self.bias is not None}, dtype={self.dtype}")
+
+    def forward(self, x) -> torch.Tensor:
+        if not isinstance(x, torch.Tensor):
+            q, s = x
+            return fp8_matmul(q, s, self.w_f8, self.w_scale, bias=self.bias, out_dtype=self.dtype)
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
+        q, s = fp8_quantize(x.reshape(-1, self.in_features).contiguous())
+        y = fp8_matmul(q, s, self.w_f8, self.w_scale, bias=self.bias, out_dtype=self.dtype)
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+
+__all__ = ["Int8MixedLinear", "Fp8BlockLinear", "Fp8RMSNorm"]

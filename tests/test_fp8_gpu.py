@@ -1,0 +1,515 @@
+"""Block-scaled e4m3 operators on the GPU, through the public entry points,
+against the 64-bit oracle (oracle/fp8_block.py).
+
+Tolerances, derived:
+  quantize   none: the oracle takes the same three fp32 roundings (scale,
+             reciprocal, product) and the e4m3 rounding, so bytes and scales
+             are equal.
+  norm, gate an fp32 value y with a relative error of at most D from 64 bits.
+             The norm's sum of squares: a chain of at most 64 fma per thread,
+             6 shuffle steps and 16 wavefront sums, all of positive terms:
+             86 * 2^-24 relative, halved by the square root; the division by
+             K, + eps, sqrt, the reciprocal and two products add at most 6
+             more half steps: D = 50 * 2^-24.  The gate: exp within 2 half
+             steps of its value, whose argument is exact, 1 + exp, the
+             division and the product: D = 8 * 2^-24.
+             A block's scale is a / 448 of the largest: D + 2^-24.  The
+             stored q is the nearest e4m3 number of y / scale: within 2^-4
+             relative, or 2^-10 absolute below the smallest normal number, of a
+             value that itself is within 2 D + 2^-22 of exact.
+  product    the matrix instruction adds the exact products of 8 consecutive
+             columns after cutting each off below 2^-13 of 2^E, E the largest
+             sum of the two factors' exponents among the 8 (a subnormal's is
+             that of 2^-6): seven products at most lose less than 2^-13 * 2^E,
+             and 2^E is at most max(|x|, 2^-6) max(|w|, 2^-6) over the 8.
+             Found with single products: beside 2^16, 2^3 is added exactly and
+             2^2 is lost at distances 1 to 7, and is not from 8 on; (1.875^2)
+             2^4 loses its last bits below 2^3.  So 7 * 2^-13 of `grain`
+             (oracle).  The 16 groups of a block and the scaled blocks are
+             added in fp32, each addition within 2^-23 (rounded or cut off) of
+             the running magnitude, with one product of scales, one with the
+             block's sum and the bias: (16 + KB + 4) * 2^-23 of the sum of
+             magnitudes.  Then half a step of Y's type, and half its smallest
+             subnormal.
+"""
+import numpy as np
+import pytest
+import torch
+
+import int8_mixed_precision_outlier_amd as i8
+from int8_mixed_precision_outlier_amd.linear import Fp8BlockLinear, Fp8RMSNorm
+from oracle import fp8_block as F
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float16, torch.bfloat16]
+E4M3 = torch.float8_e4m3fn
+
+
+def ids(t):
+    return str(t).replace("torch.", "") if isinstance(t, torch.dtype) else str(t)
+
+
+def f32(t):
+    return t.detach().float().cpu().numpy()
+
+
+def raw(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def acts(M, K, dtype, seed, std=0.5, outliers=7):
+    """Activations N(0, std^2) with a few large columns, on the GPU."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((M, K)) * std
+    for c in rng.choice(K, min(outliers, K // 16), replace=False):
+        x[:, c] *= 60
+    return torch.from_numpy(x.astype(np.float32)).to(dtype).cuda()
+
+
+def e4m3(bytes_):
+    return torch.from_numpy(np.ascontiguousarray(bytes_)).cuda().view(E4M3)
+
+
+def step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def close_blocks(q, s, y64, D, what):
+    """The device's e4m3 numbers and scales against a 64-bit row value."""
+    M, K = y64.shape
+    s = s.cpu().numpy()
+    a = np.zeros((-(-K // 128) * 128, M))
+    a[:K] = np.abs(y64).T
+    s64 = np.maximum(a.reshape(-1, 128, M).max(1), 2.0 ** -100) / 448
+    assert s.shape == s64.shape, what
+    assert np.all(np.abs(s - s64) <= (D + 2.0 ** -24) * s64), what
+    v = F.e4m3_decode(raw(q))
+    want = y64 / F.spread_columns(s, K)
+    tol = np.maximum(np.abs(want) * 2.0 ** -4, 2.0 ** -10) + (2 * D + 2.0 ** -22) * np.abs(want)
+    assert np.all(np.abs(v - want) <= tol), (what, float(np.max(np.abs(v - want) - tol)))
+
+
+ROWS = [(1, 16), (3, 112), (2, 128), (17, 144), (64, 1040), (1, 4096), (333, 4112), (5, 8208),
+        (33, 12288), (2, 65536)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,K", ROWS)
+def test_quantize_bit_exact(M, K, dtype):
+    X = acts(M, K, dtype, M * 31 + K)
+    X[0, : K // 2] = 0  # whole blocks of zeros where K allows
+    q, s = i8.fp8_quantize(X)
+    assert q.dtype == E4M3 and q.shape == (M, K) and s.shape == (-(-K // 128), M)
+    oq, os_ = F.quantize_blocks(f32(X))
+    assert np.array_equal(raw(q), oq) and np.array_equal(s.cpu().numpy(), os_)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_quantize_extremes(dtype):
+    """Subnormals, the type's largest and smallest values, signed zeros, NaN and
+    infinities, each in a block of its own and beside ordinary values."""
+    fi = torch.finfo(dtype)
+    X = torch.zeros((6, 640), dtype=dtype)
+    X[0, :128] = fi.max
+    X[0, 128:256] = fi.tiny
+    X[0, 256:384] = fi.smallest_normal * torch.finfo(dtype).eps  # smallest subnormal
+    X[0, 384] = -0.0
+    X[1] = torch.linspace(-3, 3, 640).to(dtype)
+    X[2, 5] = float("nan")
+    X[2, 6:128] = 1.5
+    X[3] = 2.0
+    X[3, 130] = float("nan")
+    X[4, 0] = fi.max
+    X[4, 1] = fi.tiny
+    q, s = i8.fp8_quantize(X.cuda())
+    oq, os_ = F.quantize_blocks(f32(X))
+    got = raw(q)
+    nan = (got & 0x7f) == 0x7f
+    assert np.array_equal(nan, np.isnan(f32(X)))
+    assert np.array_equal(got[~nan], oq[~nan]) and np.array_equal(s.cpu().numpy(), os_)
+    # an infinity: NaN in its place, an infinite scale for its block, no other block touched
+    Y = X.clone()
+    Y[1, 300] = float("-inf")
+    q2, s2 = i8.fp8_quantize(Y.cuda())
+    assert raw(q2)[1, 300] & 0x7f == 0x7f and np.isinf(s2.cpu().numpy()[2, 1])
+    keep = np.ones((6, 640), bool)
+    keep[1, 256:384] = False
+    assert np.array_equal(raw(q2)[keep], got[keep])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,K", ROWS + [(2, 2048), (2, 2064), (2, 4112), (1, 12304), (1, 16400), (1, 32784)])
+def test_rms_norm(M, K, residual, dtype):
+    X, R = acts(M, K, dtype, K + M), acts(M, K, dtype, K + M + 1)
+    g = (1 + 0.2 * acts(1, K, dtype, 5, outliers=0)[0].float()).to(dtype)
+    if M > 2:
+        X[1] = 0
+        R[1] = 0  # an all-zero row: y = 0, scales on the floor
+    r = i8.fp8_rms_norm(X, g, eps=1e-5, residual=R if residual else None)
+    h = X
+    if residual:
+        h = (X.float() + R.float()).to(dtype)
+        assert torch.equal(r[2], h)
+    y = F.rms_norm64(f32(h), f32(g), np.float64(np.float32(1e-5)))
+    close_blocks(r[0], r[1], y, 50 * 2.0 ** -24, (M, K, residual, dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_rms_norm_in_place_and_bad_values(dtype):
+    M, K = 5, 272
+    X, R, g = acts(M, K, dtype, 1), acts(M, K, dtype, 2), acts(1, K, dtype, 3)[0]
+    want = i8.fp8_rms_norm(X, g, residual=R)
+    R2 = R.clone()
+    got = i8.fp8_rms_norm(X, g, residual=R2, residual_out=R2)
+    assert got[2].data_ptr() == R2.data_ptr()
+    X2 = X.clone()
+    into_x = i8.fp8_rms_norm(X2, g, residual=R, residual_out=X2)
+    same = i8.fp8_rms_norm(X, g, residual=X)  # the same tensor twice
+    assert torch.equal(same[2], (2 * X.float()).to(dtype))
+    for other in (got, into_x):
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(want, other))
+    # a NaN spoils its own row only
+    Xn = X.clone()
+    Xn[3, 7] = float("nan")
+    q, s, h = i8.fp8_rms_norm(Xn, g, residual=R)
+    assert np.all(raw(q)[3] & 0x7f == 0x7f)
+    rows = [0, 1, 2, 4]
+    assert np.array_equal(raw(q)[rows], raw(want[0])[rows]) and torch.equal(s[:, rows], want[1][:, rows])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 144), (17, 1040), (130, 5120), (1, 20480), (2, 65536)])
+def test_silu_mul(M, K, dtype):
+    GU = acts(M, 2 * K, dtype, K, std=2.0, outliers=3)
+    GU[0, 0], GU[0, 1] = -100.0, 100.0  # exp overflows, exp underflows
+    q, s = i8.fp8_silu_mul(GU)
+    close_blocks(q, s, F.silu_mul64(f32(GU)), 8 * 2.0 ** -24, (M, K, dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("K,N", [(16, 16), (128, 128), (144, 272), (272, 144), (1040, 400)])
+def test_quantize_and_pack_weight(K, N, dtype):
+    W = acts(K, N, dtype, N, std=0.02)
+    W[:16, :16] = 0
+    w, ws = i8.fp8_quantize_weight(W)
+    oq, os_ = F.quantize_weight_blocks(f32(W))
+    assert np.array_equal(raw(w), F.pack_weight(oq)) and np.array_equal(ws.cpu().numpy(), os_)
+    assert torch.equal(i8.fp8_pack_weight(e4m3(oq)).view(torch.uint8), w.view(torch.uint8))
+
+
+def operands(M, K, N, seed, spread=1.0):
+    """Random e4m3 operands with every code in use and scales over some binades."""
+    rng = np.random.default_rng(seed)
+    code = lambda *s: (rng.integers(0, 127, s) | (rng.integers(0, 2, s) << 7)).astype(np.uint8)  # noqa: E731
+    kb, nb = -(-K // 128), -(-N // 128)
+    xs = (2.0 ** rng.uniform(-8 - spread, -8 + spread, (kb, M))).astype(np.float32)
+    ws = (2.0 ** rng.uniform(-12 - spread, -12 + spread, (nb, kb))).astype(np.float32)
+    return code(M, K), xs, code(N, K), ws
+
+
+def on_gpu(xq, xs, wq, ws):
+    return e4m3(xq), torch.from_numpy(xs).cuda(), i8.fp8_pack_weight(e4m3(wq)), torch.from_numpy(ws).cuda()
+
+
+def check_product(Y, oracle, K, dtype, what):
+    want, mag, grain = oracle
+    Y = Y.detach().double().cpu().numpy()
+    kb = -(-K // 128)
+    tol = 7 * 2.0 ** -13 * grain + (16 + kb + 4) * 2.0 ** -23 * mag
+    tol = tol + step(dtype) * (np.abs(want) + tol)
+    tol = tol + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2
+    bad = np.abs(Y - want) - tol
+    assert np.all(bad <= 0), (what, float(bad.max()), float(np.max(np.abs(Y - want) / np.maximum(mag, 1e-300))))
+
+
+PRODUCTS = [(1, 16, 16), (1, 128, 16), (2, 112, 48), (3, 144, 144), (15, 256, 272), (16, 400, 128),
+            (17, 1040, 144), (31, 512, 528), (33, 144, 1040), (48, 2048, 256), (64, 384, 400),
+            (65, 640, 256), (77, 5136, 272), (127, 1152, 128), (128, 128, 384), (129, 272, 640),
+            (200, 4096, 144), (257, 528, 1040), (300, 1536, 784), (1, 12288, 4096), (7, 4112, 4112),
+            (515, 640, 2064)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,K,N", PRODUCTS)
+def test_matmul(M, K, N, dtype):
+    xq, xs, wq, ws = operands(M, K, N, M * 7 + K + N)
+    b = torch.randn(N, generator=torch.Generator().manual_seed(N)).to(dtype)
+    args = on_gpu(xq, xs, wq, ws)
+    for bias in (None, b):
+        want = F.matmul64(xq, xs, wq, ws, None if bias is None else f32(bias))
+        Y = i8.fp8_matmul(*args, bias=None if bias is None else bias.cuda(), out_dtype=dtype)
+        assert Y.dtype == dtype
+        check_product(Y, want, K, dtype, (M, K, N, bias is not None))
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 144, 64), (16, 2064, 272), (40, 528, 400), (150, 1024, 528), (513, 272, 784)])
+def test_matmul_exact_small_integers(M, K, N):
+    """Integers -4 .. 4 with unit scales: every partial sum is exact in fp32, so
+    the product is the integer one, in every place."""
+    rng = np.random.default_rng(K)
+    x, w = rng.integers(-4, 5, (M, K)), rng.integers(-4, 5, (N, K))
+    ones = lambda *s: np.ones(s, np.float32)  # noqa: E731
+    args = on_gpu(F.e4m3_encode(x), ones(-(-K // 128), M), F.e4m3_encode(w), ones(-(-N // 128), -(-K // 128)))
+    Y = i8.fp8_matmul(*args, out_dtype=torch.float16).cpu().numpy()
+    assert np.array_equal(Y, (x @ w.T).astype(np.float16))
+
+
+@pytest.mark.parametrize("M", [2, 40, 200])
+def test_matmul_bad_rows_stay_alone(M):
+    """NaN in one token, an infinite scale in another: their rows are NaN (or
+    infinite), no others, with K ending inside a block, where a tile's columns
+    past K are the next token's."""
+    K, N = 400, 272
+    xq, xs, wq, ws = operands(M, K, N, 9)
+    clean = i8.fp8_matmul(*on_gpu(xq, xs, wq, ws), out_dtype=torch.bfloat16)
+    xq2, xs2 = xq.copy(), xs.copy()
+    xq2[1, 0] = 0x7f
+    xs2[2 % M, M - 1] = np.inf
+    Y = i8.fp8_matmul(*on_gpu(xq2, xs2, wq, ws), out_dtype=torch.bfloat16)
+    assert bool(torch.isnan(Y[1]).all())
+    rest = [m for m in range(M) if m not in (1, M - 1)]
+    assert torch.equal(Y[rest], clean[rest])
+    assert not bool(torch.isfinite(Y[M - 1]).any())
+
+
+def test_matmul_scales_of_all_sizes():
+    """Scales from 2^-60 to 2^40, a zero scale, and e4m3 subnormals."""
+    M, K, N = 20, 512, 144
+    xq, xs, wq, ws = operands(M, K, N, 4)
+    xs *= (2.0 ** np.linspace(-60, 40, M)).astype(np.float32)
+    xs[1, 3] = 0.0
+    xq[5] &= 0x87  # subnormal numbers only
+    want = F.matmul64(xq, xs, wq, ws)
+    Y = i8.fp8_matmul(*on_gpu(xq, xs, wq, ws), out_dtype=torch.bfloat16)
+    check_product(Y, want, K, torch.bfloat16, "scales")
+
+
+def test_empty_sizes():
+    e = lambda *s, d=E4M3: torch.empty(s, dtype=d, device="cuda")  # noqa: E731
+    f = torch.float32
+    b = torch.arange(32, dtype=torch.bfloat16, device="cuda")
+    Y = i8.fp8_matmul(e(3, 0), e(0, 3, d=f), e(32, 0), e(1, 0, d=f), bias=b)
+    assert torch.equal(Y, b.expand(3, 32))
+    assert not i8.fp8_matmul(e(3, 0), e(0, 3, d=f), e(32, 0), e(1, 0, d=f)).any()
+    assert i8.fp8_matmul(e(0, 128), e(1, 0, d=f), e(32, 128), e(1, 1, d=f)).shape == (0, 32)
+    assert i8.fp8_matmul(e(3, 128), e(1, 3, d=f), e(0, 128), e(0, 1, d=f)).shape == (3, 0)
+    q, s = i8.fp8_quantize(e(0, 256, d=torch.float16))
+    assert q.shape == (0, 256) and s.shape == (2, 0)
+    q, s, h = i8.fp8_rms_norm(e(0, 64, d=torch.float16), e(64, d=torch.float16), residual=e(0, 64, d=torch.float16))
+    assert h.shape == (0, 64)
+    assert i8.fp8_silu_mul(e(4, 0, d=torch.float16))[0].shape == (4, 0)
+    w, ws = i8.fp8_quantize_weight(e(0, 16, d=torch.float16))
+    assert w.shape == (16, 0) and ws.shape == (1, 0)
+
+
+def test_refusals():
+    x = torch.zeros((4, 256), dtype=torch.float16, device="cuda")
+    q, s = i8.fp8_quantize(x)
+    w, ws = i8.fp8_quantize_weight(torch.zeros((256, 32), dtype=torch.float16, device="cuda"))
+    bad = [
+        (TypeError, lambda: i8.fp8_quantize(x.float())),
+        (ValueError, lambda: i8.fp8_quantize(x[:, ::2])),
+        (ValueError, lambda: i8.fp8_quantize(x[0])),
+        (i8.Int8mmError, lambda: i8.fp8_quantize(x[:, :40].contiguous())),
+        (i8.Int8mmError, lambda: i8.fp8_quantize(x.view(-1)[4:4 + 256].view(1, 256))),  # misaligned rows
+        (TypeError, lambda: i8.fp8_rms_norm(x, x[0].bfloat16())),
+        (ValueError, lambda: i8.fp8_rms_norm(x, x[0, :128])),
+        (TypeError, lambda: i8.fp8_rms_norm(x, x[0], residual=x.bfloat16())),
+        (ValueError, lambda: i8.fp8_rms_norm(x, x[0], residual=x[:2])),
+        (ValueError, lambda: i8.fp8_rms_norm(x, x[0], residual_out=x)),
+        (i8.Int8mmError, lambda: i8.fp8_rms_norm(x, x[0], eps=0.0)),
+        (ValueError, lambda: i8.fp8_silu_mul(x[:, :255].contiguous())),
+        (ValueError, lambda: i8.fp8_matmul(q, s.t().contiguous(), w, ws)),
+        (ValueError, lambda: i8.fp8_matmul(q, s, w[:, :128].contiguous(), ws)),
+        (ValueError, lambda: i8.fp8_matmul(q, s, w, ws.t().contiguous())),
+        (TypeError, lambda: i8.fp8_matmul(q, s.half(), w, ws)),
+        (TypeError, lambda: i8.fp8_matmul(q.view(torch.int8), s, w, ws)),
+        (TypeError, lambda: i8.fp8_matmul(q, s, w, ws, out_dtype=torch.float32)),
+        (TypeError, lambda: i8.fp8_matmul(q, s, w, ws, bias=ws[0, :1].expand(32).contiguous())),
+        (ValueError, lambda: i8.fp8_matmul(q, s, w, ws, bias=x[0])),
+        (ValueError, lambda: i8.fp8_matmul(q, s, w, ws, out=x.bfloat16())),
+        (ValueError, lambda: i8.fp8_quantize(x, out=(q[:2], s))),
+    ]
+    for k, (err, call) in enumerate(bad):
+        with pytest.raises(err):
+            call()
+            pytest.fail(f"refusal {k} did not raise")
+
+
+def test_given_outputs_and_results_carry_no_gradient():
+    x = acts(9, 400, torch.bfloat16, 1)
+    q, s = i8.fp8_quantize(x)
+    out = (torch.zeros_like(q), torch.zeros_like(s))
+    r = i8.fp8_quantize(x, out=out)
+    assert r[0] is out[0] and r[1] is out[1] and torch.equal(out[0].view(torch.uint8), q.view(torch.uint8))
+    w, ws = i8.fp8_quantize_weight(acts(400, 64, torch.bfloat16, 2))
+    y = torch.full((9, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert i8.fp8_matmul(q, s, w, ws, out=y) is y
+    assert torch.equal(y, i8.fp8_matmul(q, s, w, ws))
+    xg = x.clone().requires_grad_()
+    assert not i8.fp8_rms_norm(xg, x[0].contiguous())[1].requires_grad
+    # memory behind the outputs is left as it was
+    big = torch.full((11, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    i8.fp8_matmul(q, s, w, ws, out=big[:9])
+    assert bool((big[9:] == 3).all()) and torch.equal(big[:9], y)
+
+
+def ffn(x, res, g, up, down):
+    q, s, h = i8.fp8_rms_norm(x, g, residual=res)
+    gu = i8.fp8_matmul(q, s, *up, out_dtype=x.dtype)
+    a, as_ = i8.fp8_silu_mul(gu)
+    return q, s, h, gu, a, as_, i8.fp8_matmul(a, as_, *down, out_dtype=x.dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M", [1, 19, 160])
+def test_feed_forward_chain(M, dtype):
+    """Norm, gate-and-up product, gated activation, down product in a row, each
+    stage against 64 bits from the stage before, then the whole against the
+    feed-forward in 64 bits on the unquantized weights."""
+    K, I = 528, 784
+    x, res = acts(M, K, dtype, 1), acts(M, K, dtype, 2)
+    g = (1 + 0.1 * acts(1, K, dtype, 3, outliers=0)[0].float()).to(dtype)
+    Wu, Wd = acts(K, 2 * I, dtype, 4, std=0.05, outliers=0), acts(I, K, dtype, 5, std=0.05, outliers=0)
+    up, down = i8.fp8_quantize_weight(Wu), i8.fp8_quantize_weight(Wd)
+    q, s, h, gu, a, as_, y = ffn(x, res, g, up, down)
+    y64 = F.rms_norm64(f32(h), f32(g), np.float64(np.float32(1e-6)))
+    close_blocks(q, s, y64, 50 * 2.0 ** -24, "norm")
+    uq, us = F.quantize_weight_blocks(f32(Wu))
+    dq, ds = F.quantize_weight_blocks(f32(Wd))
+    want = F.matmul64(raw(q), s.cpu().numpy(), uq, us)
+    check_product(gu, want, K, dtype, "up")
+    close_blocks(a, as_, F.silu_mul64(f32(gu)), 8 * 2.0 ** -24, "gate")
+    want = F.matmul64(raw(a), as_.cpu().numpy(), dq, ds)
+    check_product(y, want, I, dtype, "down")
+    whole = F.silu_mul64(y64 @ f32(Wu).astype(np.float64)) @ f32(Wd).astype(np.float64)
+    # four e4m3 roundings (2^-4 at most, uniform: /sqrt(3)) of independent
+    # terms each, and the gate's: well below 0.1 of the norm
+    err = np.linalg.norm(f32(y) - whole) / np.linalg.norm(whole)
+    assert err < 0.1, err
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_modules(dtype):
+    K, N = 272, 144
+    lin = torch.nn.Linear(K, N, dtype=dtype, device="cuda")
+    layer = Fp8BlockLinear.from_linear(lin)
+    x = acts(6, K, dtype, 3).view(2, 3, K)
+    y = layer(x)
+    assert y.shape == (2, 3, N) and y.dtype == dtype and not y.requires_grad
+    q, s = i8.fp8_quantize(x.view(6, K))
+    assert torch.equal(layer((q, s)).view(2, 3, N), y)
+    wq, ws = F.quantize_weight_blocks(f32(lin.weight).T)
+    want = F.matmul64(raw(q), s.cpu().numpy(), wq, ws, f32(lin.bias))
+    check_product(y.view(6, N), want, K, dtype, "layer")
+    again = Fp8BlockLinear.from_quantized(e4m3(wq), torch.from_numpy(ws).cuda(), lin.bias, dtype)
+    assert torch.equal(again(x), y)
+    norm = Fp8RMSNorm(torch.ones(K, dtype=dtype, device="cuda"))
+    (q, s), h = norm(x, x)
+    assert h.shape == x.shape and torch.equal(h, (2 * x.float()).to(dtype))
+    assert torch.equal(layer(norm(h)), layer((q, s)))
+    with pytest.raises(ValueError):
+        layer(x[..., :16])
+    with pytest.raises(ValueError):
+        norm(x, x[:1])
+    state = Fp8BlockLinear.from_linear(torch.nn.Linear(K, N, dtype=dtype, device="cuda"))
+    state.load_state_dict(layer.state_dict())
+    assert torch.equal(state(x), y)
+
+
+def test_graph_replays():
+    """The chain captured once and replayed with new inputs, eager work between."""
+    K, I, M = 528, 784, 5
+    x, res = acts(M, K, torch.bfloat16, 1), acts(M, K, torch.bfloat16, 2)
+    g = acts(1, K, torch.bfloat16, 3)[0]
+    up = i8.fp8_quantize_weight(acts(K, 2 * I, torch.bfloat16, 4, std=0.05))
+    down = i8.fp8_quantize_weight(acts(I, K, torch.bfloat16, 5, std=0.05))
+    ffn(x, res, g, up, down)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ffn(x, res, g, up, down)
+    for k in range(4):
+        x.copy_(acts(M, K, torch.bfloat16, 10 + k))
+        res.copy_(acts(M, K, torch.bfloat16, 20 + k))
+        graph.replay()
+        want = ffn(x, res, g, up, down)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(out, want)), k
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each of other sizes, give what they
+    give alone; a given stream is the one that is used."""
+    def work(M, K, N, seed, stream=None):
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(0):
+            x = acts(M, K, torch.float16, seed)
+            w = i8.fp8_quantize_weight(acts(K, N, torch.float16, seed + 1, std=0.05))
+            if stream is not None:
+                stream.synchronize()
+            return [i8.fp8_matmul(*i8.fp8_quantize(x, stream=stream), *w, out_dtype=torch.float16,
+                                  stream=stream) for _ in range(10)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    ra, rb = work(40, 2048, 2064, 1, a), work(300, 1040, 1024, 3, b)
+    torch.cuda.synchronize()
+    wa, wb = work(40, 2048, 2064, 1), work(300, 1040, 1024, 3)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, wa[0]) for y in ra + wa) and all(torch.equal(y, wb[0]) for y in rb + wb)
+
+
+def test_results_do_not_change_between_runs():
+    xq, xs, wq, ws = operands(70, 4112, 1040, 11)
+    args = on_gpu(xq, xs, wq, ws)
+    first = i8.fp8_matmul(*args)
+    assert all(torch.equal(i8.fp8_matmul(*args), first) for _ in range(5))
+
+
+def codes(n, seed):
+    """n finite e4m3 codes on the GPU, without host memory."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(0, 127, (n,), generator=g, device="cuda", dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("M,N", [(1, 32768), (40, 32768), (32768, 16), (130, 32768)])
+def test_matmul_at_the_size_limit(M, N):
+    """Operands of 2^31 bytes: offsets past 31 bits, checked on the last rows
+    and features against 64 bits."""
+    K = 65536
+    x = codes(M * K, 1).view(M, K)
+    w = codes(N * K, 2).view(N, K)
+    xs = torch.rand((K // 128, M), device="cuda") * 1e-3
+    ws = torch.rand((-(-N // 128), K // 128), device="cuda") * 1e-3
+    Y = i8.fp8_matmul(x.view(E4M3), xs, i8.fp8_pack_weight(w.view(E4M3)), ws)
+    m, n = max(0, M - 3), N - 16
+    want = F.matmul64(raw(x[m:]), xs[:, m:].cpu().numpy(), raw(w[n:]),
+                           ws[-1:].cpu().numpy())
+    check_product(Y[m:, n:], want, K, torch.bfloat16, (M, N))
+
+
+def test_row_operators_at_the_size_limit():
+    """2^31 elements in, more rows than one launch takes: the last rows."""
+    for M, K in ((32768, 65536), (1 << 24, 128), (1 << 21, 16)):
+        X = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+        X[: M // 2] = 1.0
+        X[M // 2:] = 2.0
+        X[-3:] = acts(3, K, torch.bfloat16, 1)
+        q, s = i8.fp8_quantize(X)
+        oq, os_ = F.quantize_blocks(f32(X[-3:]))
+        assert np.array_equal(raw(q[-3:]), oq) and np.array_equal(s[:, -3:].cpu().numpy(), os_)
+        assert bool((s[:, : M // 2] == s[0, 0]).all()) and bool((q[: M // 2].view(torch.uint8) == 0x7e).all())
+        assert bool((s[:, M // 2: -3] == s[0, M // 2]).all())
+        g = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+        q, s, h = i8.fp8_rms_norm(X, g, residual=X, residual_out=X)
+        y = F.rms_norm64(f32(X[-3:]), f32(g), np.float64(np.float32(1e-6)))
+        close_blocks(q[-3:], s[:, -3:].contiguous(), y, 50 * 2.0 ** -24, (M, K))
+        assert bool((h[: M // 2] == 2).all()) and bool((s[:, : M // 2] == s[0, 0]).all())
+        del X, q, s, h
+        if K >= 32:
+            GU = torch.ones((M, K), dtype=torch.bfloat16, device="cuda")
+            GU[-2:] = acts(2, K, torch.bfloat16, 2)
+            q, s = i8.fp8_silu_mul(GU)
+            close_blocks(q[-2:], s[:, -2:].contiguous(), F.silu_mul64(f32(GU[-2:])), 8 * 2.0 ** -24, (M, K))
+            del GU, q, s
+        torch.cuda.empty_cache()
