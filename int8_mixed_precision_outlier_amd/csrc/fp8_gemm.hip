@@ -22,6 +22,7 @@
 #include "fp8.hpp"
 
 #include <atomic>
+#include <utility>
 
 namespace i8mm {
 
@@ -31,34 +32,76 @@ constexpr int kMaxKB = 65536 / kFp8Block;
 // A buffer offset past every operand (they hold at most 2^31 bytes).
 constexpr uint32_t kOutOfRange = 0xffffff00u;
 
-// Four values of one token at features n .. n+3 (n % 4 == 0, N % 16 == 0).
+// LDS of a tile: two stages of one K block each (W's half blocks, then X's
+// rows), the token scales [stage][wavefront][its tokens], the tile's weight
+// scales [128-feature block][KB].
+template <int BM, int BN, int WM, int WN>
+struct GemmLds {
+  static constexpr int STAGE = (BM + BN) * 128;
+  static constexpr int SX = 2 * STAGE;
+  static constexpr int SW = SX + 2 * WN * BM * 4;
+  static constexpr int NBT = BN > 128 ? BN / 128 : 1;
+  static constexpr int MAX = SW + NBT * kMaxKB * 4;
+  static_assert(MAX <= 160 * 1024, "LDS budget");
+};
+
+// Order of one feature block's instructions: each of its MFMAs followed by
+// four fmas, then LDS reads (R0 after the first, R1 after each of the others)
+// and an even share of V DMAs.
+constexpr int kSgMfma = 0x008, kSgValu = 0x002, kSgDsRead = 0x100, kSgVmemRead = 0x020;
+template <int R0, int R1, int V, int... Js>
+__device__ __forceinline__ void order_impl(std::integer_sequence<int, Js...>) {
+  constexpr int FM = sizeof...(Js);
+  ((__builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0),
+    __builtin_amdgcn_sched_group_barrier(kSgValu, 4, 0),
+    __builtin_amdgcn_sched_group_barrier(kSgDsRead, Js == 0 ? R0 : R1, 0),
+    __builtin_amdgcn_sched_group_barrier(kSgVmemRead, (Js + 1) * V / FM - Js * V / FM, 0)),
+   ...);
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <int FM, int R0, int R1, int V>
+__device__ __forceinline__ void order() {
+  order_impl<R0, R1, V>(std::make_integer_sequence<int, FM>{});
+}
+
+template <class F, int... Is>
+__device__ __forceinline__ void unroll(F&& f, std::integer_sequence<int, Is...>) {
+  (f(std::integral_constant<int, Is>{}), ...);
+}
+
+// Two 16x16 blocks of adjacent features (nb .. nb+15 in ya, nb+16 .. +31 in
+// yb) of the same 16 tokens as one 16-byte store per lane: swapping rows 1
+// and 3 of the first with rows 0 and 2 of the second leaves 8 consecutive
+// features of a token in each lane.  N % 16 == 0, so they are all in range or
+// all out.
 template <int T>
-__device__ __forceinline__ void store4(const v4f& y, int n, int m, int M, int N,
-                                       uint16_t* __restrict__ Y) {
+__device__ __forceinline__ void store32(const v4f& ya, const v4f& yb, int nb, int mb, int M, int N,
+                                        uint16_t* __restrict__ Y) {
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const auto lo = __builtin_amdgcn_permlane16_swap(pack16x2<T>(ya[0], ya[1]),
+                                                   pack16x2<T>(yb[0], yb[1]), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(pack16x2<T>(ya[2], ya[3]),
+                                                   pack16x2<T>(yb[2], yb[3]), false, false);
+  const int m = mb + (lane & 15), n = nb + 8 * (q >> 1) + 16 * (q & 1);
   if (m < M && n < N)
-    *reinterpret_cast<uint2*>(Y + (size_t)m * N + n) =
-        make_uint2(pack16x2<T>(y[0], y[1]), pack16x2<T>(y[2], y[3]));
+    *reinterpret_cast<uint4*>(Y + (size_t)m * N + n) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
 }
 
 }  // namespace
 
-template <int T, int BM, int BN, int WM, int WN, int STAGES>
+template <int T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     const uint8_t* __restrict__ X, const float* __restrict__ xs, const uint8_t* __restrict__ W,
     const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y,
     int M, int N, int K, int KB, int tilesM, int tilesN, int groupM) {
+  using L = GemmLds<BM, BN, WM, WN>;
   constexpr int NWAVE = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int FM = WTM / 16, FN = WTN / 16;
-  constexpr int STAGE = (BM + BN) * 128;
-  constexpr int WDMA = BN / 8, XDMA = BM / 8;  // 1 KB DMA instructions of a stage
-  constexpr int DPW = (WDMA + XDMA) / NWAVE;
-  constexpr int SDMA = WTM / 64;  // DMA instructions of a wavefront's token scales
-  static_assert((WDMA + XDMA) % NWAVE == 0 && WTM % 64 == 0 && 128 % WTN == 0, "tiling");
-  constexpr int OPS = DPW + SDMA;  // DMA instructions of a wavefront per stage
-  constexpr int SX = STAGES * STAGE;                  // token scales: [stage][wavefront][WTM]
-  constexpr int SW = SX + STAGES * NWAVE * WTM * 4;   // weight scales: [wn block][KB]
-  constexpr int NBT = BN > 128 ? BN / 128 : 1;        // scale blocks across the tile
+  constexpr int WDMA = BN / 8 / NWAVE, XDMA = BM / 8 / NWAVE;  // 1 KB DMAs of a wavefront per stage
+  constexpr int SDMA = WTM / 64;                               // and those of its token scales
+  static_assert(BN / 8 % NWAVE == 0 && BM / 8 % NWAVE == 0 && WTM % 64 == 0, "DMA split");
+  static_assert(128 % WTN == 0 && FN % 2 == 0 && FM >= 4, "a wavefront's features share a scale block");
   extern __shared__ __align__(16) int8_t smem[];
 
   const int Tt = tilesM * tilesN;
@@ -77,62 +120,66 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   const int nrb = N >> 4;
   const int q4 = lane >> 4, r16 = lane & 15;
 
-  // the tile's weight scales (rows past the last 128-feature block repeat it:
+  // the tile's weight scales (blocks past the last 128 features repeat it:
   // they only feed outputs that are never stored)
-  float* sw = reinterpret_cast<float*>(smem + SW);
+  float* sw = reinterpret_cast<float*>(smem + L::SW);
   const int nbs = (N + kFp8Block - 1) / kFp8Block;
-  for (int i = t; i < NBT * KB; i += NWAVE * 64) {
+  for (int i = t; i < L::NBT * KB; i += NWAVE * 64) {
     const int nb = min(n0 / kFp8Block + i / KB, nbs - 1);
     sw[i] = ws[(size_t)nb * KB + i % KB];
   }
   const float* my_sw = sw + (wn * WTN / 128) * KB;
 
-  // this wavefront's DMA sources: 1 KB pieces J = w*DPW + j of a stage, the
-  // weight's first.  Rows past N or M are clamped to the last valid one:
-  // they only feed outputs that are never stored.
-  uint32_t src[DPW];
-  bool isw[DPW];
+  // DMA sources of this wavefront: WDMA half blocks of W and XDMA pieces of 8
+  // rows of X.  Rows past N or M are clamped to the last valid one: they
+  // only feed outputs that are never stored.
   const int xrow = lane >> 3;
-  const uint32_t chunk = (lane & 7) ^ (xrow & 7);  // the column chunk of this lane's X pieces
+  const uint32_t chunk = (lane & 7) ^ xrow;  // the column chunk of this lane's X pieces
+  uint32_t wsrc[WDMA], xsrc[XDMA];
 #pragma unroll
-  for (int j = 0; j < DPW; ++j) {
-    const int J = w * DPW + j;
-    isw[j] = J < WDMA;
-    if (isw[j]) {
-      const int rb = min(n0 / 16 + J / 2, nrb - 1);
-      src[j] = (uint32_t)rb * (uint32_t)KB * 2048u + (J & 1) * 1024u + lane * 16u;
-    } else {
-      const int r = (J - WDMA) * 8 + xrow;
-      const int row = min(m0 + r, M - 1);
-      src[j] = (uint32_t)row * (uint32_t)K + chunk * 16u;
-    }
+  for (int j = 0; j < WDMA; ++j) {
+    const int J = w * WDMA + j;
+    const int rb = min(n0 / 16 + J / 2, nrb - 1);
+    wsrc[j] = __builtin_amdgcn_readfirstlane((uint32_t)rb * (uint32_t)KB * 2048u + (J & 1) * 1024u);
   }
+#pragma unroll
+  for (int j = 0; j < XDMA; ++j) {
+    const int row = min(m0 + (w * XDMA + j) * 8 + xrow, M - 1);
+    xsrc[j] = (uint32_t)row * (uint32_t)K + chunk * 16u;
+  }
+  const int mw = min(m0 + wm * WTM, M - 1);
   const uint32_t wbytes = (uint32_t)nrb * (uint32_t)KB * 2048u;
   const uint32_t xbytes = (uint32_t)M * (uint32_t)K;
 
-  // DMAs of K block kb into its stage.  Blocks at or past KB get empty
-  // descriptors (zeros).  In a last block that K ends inside, chunks at or
-  // past K read from an offset out of every range (zeros).
-  auto dma = [&](int kb, int stage) {
+  // This wavefront's DMAs of K block kb.  Blocks at or past KB get empty
+  // descriptors (zeros), so the loop needs no branch.  In a last block that
+  // K ends inside, chunks at or past K read from an offset out of every
+  // range (zeros); tokens past M read zero scales.
+  constexpr int OPS = WDMA + XDMA + SDMA;
+  auto dma = [&](int kb, int stage, int d0, int d1) {
     const bool live = kb < KB;
-    const uint32_t k0 = live ? (uint32_t)kb : 0u;
+    const int k = live ? kb : 0;
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(W + (size_t)k0 * 2048), (short)0, live ? (int)(wbytes - k0 * 2048u) : 0, 0x00020000);
+        (void*)W, (short)0, live ? (int)wbytes : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(X + (size_t)k0 * 128), (short)0, live ? (int)(xbytes - k0 * 128u) : 0, 0x00020000);
-    const bool out = k0 * 128u + chunk * 16u >= (uint32_t)K;
-    int8_t* dst = smem + stage * STAGE + w * DPW * 1024;
-#pragma unroll
-    for (int j = 0; j < DPW; ++j) {
-      dma16(isw[j] ? rw : rx, dst + j * 1024, (int)(out && !isw[j] ? kOutOfRange : src[j]), 0);
-    }
-    // scales of the wavefront's tokens (lanes past M read zeros)
-    const int mw = min(m0 + wm * WTM, M - 1);
+        (void*)X, (short)0, live ? (int)xbytes : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(xs + (size_t)k0 * M + mw), (short)0, live ? min(M - mw, WTM) * 4 : 0, 0x00020000);
+        (void*)(xs + (size_t)k * M + mw), (short)0, live ? min(M - mw, WTM) * 4 : 0, 0x00020000);
+    const bool out = (uint32_t)k * 128u + chunk * 16u >= (uint32_t)K;
+    int8_t* base = smem + stage * L::STAGE;
 #pragma unroll
-    for (int s = 0; s < SDMA; ++s)
-      dma4(rs, smem + SX + ((stage * NWAVE + w) * WTM + s * 64) * 4, lane * 4 + s * 256, 0);
+    for (int d = d0; d < d1; ++d) {
+      if (d < WDMA) {
+        dma16(rw, base + (w * WDMA + d) * 1024, lane * 16, (int)(wsrc[d] + (uint32_t)k * 2048u));
+      } else if (d < WDMA + XDMA) {
+        const int j = d - WDMA;
+        dma16(rx, base + BN * 128 + (w * XDMA + j) * 1024, (int)(out ? kOutOfRange : xsrc[j]),
+              k * 128);
+      } else {
+        const int j = d - WDMA - XDMA;
+        dma4(rs, smem + L::SX + ((stage * NWAVE + w) * WTM + j * 64) * 4, lane * 4 + j * 256, 0);
+      }
+    }
   };
 
   v4f acc[FN][FM];
@@ -141,97 +188,146 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = v4f{};
 
+  // Operand fragments: two weight fragments (the next feature block's loaded
+  // under the current one's MFMAs), the tokens' FM fragments and scales of
+  // the current K block; and the last four partial products, each scaled in
+  // kLag MFMAs after its own.
+  constexpr int kLag = 3;
+  v8i fw[2], fx[FM];
+  float sx[FM], s[FM] = {};
+  float s_w = 0.0f;
+  v4f p[4] = {};
+  const int8_t* wb = smem + (wn * WTN / 16) * 2048 + lane * 16;
+  const int8_t* xb = smem + BN * 128 + (wm * WTM + r16) * 128;
+  const int xlo = (q4 ^ (r16 & 7)) * 16, xhi = ((q4 + 4) ^ (r16 & 7)) * 16;
+  auto read_w = [&](int stage, int i, v8i& f) {
+    const int8_t* q = wb + stage * L::STAGE + i * 2048;
+    const v4i lo = *reinterpret_cast<const v4i*>(q);
+    const v4i hi = *reinterpret_cast<const v4i*>(q + 1024);
+    f = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto read_x = [&](int stage, int j, v8i& f) {
+    const int8_t* q = xb + stage * L::STAGE + j * 2048;
+    const v4i lo = *reinterpret_cast<const v4i*>(q + xlo);
+    const v4i hi = *reinterpret_cast<const v4i*>(q + xhi);
+    f = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto read_s = [&](int stage, int kb) {
+    const float* q = reinterpret_cast<const float*>(smem + L::SX) + (stage * NWAVE + w) * WTM + r16;
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) dma(s, s);
-  __syncthreads();  // the weight scales (and, conservatively, the first DMAs)
+    for (int j = 0; j < FM; ++j) sx[j] = q[j * 16];
+    s_w = my_sw[kb];
+  };
+  auto scale_in = [&](int i, int j, const v4f& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(v[e], s[j], acc[i][j][e]);
+  };
 
-  int stage = 0;
+  if (KB > 0) {
+    dma(0, 0, 0, OPS);
+    __syncthreads();  // the weight scales and the first stage
+    read_s(0, 0);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) read_x(0, j, fx[j]);
+    read_w(0, 0, fw[0]);
+  }
   for (int kb = 0; kb < KB; ++kb) {
-    // K block kb landed in every wavefront, and every wavefront is done with
-    // the stage of kb - 1, which the next DMA overwrites
-    barrier_vm<(STAGES - 2) * OPS>();
-    dma(kb + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-    const int8_t* wb = smem + stage * STAGE + (wn * WTN / 16) * 2048 + lane * 16;
-    const int8_t* xb = smem + stage * STAGE + BN * 128 + wm * WTM * 128;
-    const float* sb = reinterpret_cast<const float*>(smem + SX) + (stage * NWAVE + w) * WTM;
-    const float s_w = my_sw[kb];
-    v8i fx[FM];
-    float s[FM];
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int8_t* p = xb + (j * 16 + r16) * 128;
-      const v4i lo = *reinterpret_cast<const v4i*>(p + ((q4 ^ (r16 & 7)) * 16));
-      const v4i hi = *reinterpret_cast<const v4i*>(p + (((q4 + 4) ^ (r16 & 7)) * 16));
-      fx[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      s[j] = sb[j * 16 + r16] * s_w;
-    }
-#pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      const v4i lo = *reinterpret_cast<const v4i*>(wb + i * 2048);
-      const v4i hi = *reinterpret_cast<const v4i*>(wb + i * 2048 + 1024);
-      const v8i fw = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    const int st = kb & 1;
+    // feature block i of K block kb; `with(j)` issues loads after MFMA j
+    auto group = [&](auto I, auto&& with) {
+      constexpr int i = decltype(I)::value;
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
-        const v4f p = mfma16_e4m3(fw, fx[j]);
+        const int n = i * FM + j, o = (n + FN * FM - kLag) % (FN * FM);
+        p[n & 3] = mfma16_e4m3(fw[i & 1], fx[j]);
+        if (n == kLag) {  // the previous block's products are all in
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s[j], acc[i][j][e]);
+          for (int q = 0; q < FM; ++q) s[q] = sx[q] * s_w;
+        }
+        scale_in(o / FM, o % FM, p[o & 3]);
+        with(j);
       }
-    }
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    };
+    auto upto = [&](auto I) {
+      constexpr int i = decltype(I)::value;
+      // K block kb + 1 goes into the other stage, free since the last
+      // barrier, its DMAs spread over the first two feature blocks
+      constexpr int v0 = i == 0 ? 0 : (OPS + 1) / 2, v1 = i == 0 ? (OPS + 1) / 2 : OPS;
+      group(I, [&](int j) {
+        if (j == 0) read_w(st, i + 1, fw[(i + 1) & 1]);
+      });
+      if constexpr (i < 2) dma(kb + 1, st ^ 1, v0, v1);
+      order<FM, 2, 0, i < 2 ? v1 - v0 : 0>();
+    };
+    unroll(upto, std::make_integer_sequence<int, FN - 1>{});
+    // every wavefront has read all of K block kb's stage, and its own DMAs of
+    // kb + 1 have landed: that stage may be overwritten, the other be read
+    barrier_vm<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    group(std::integral_constant<int, FN - 1>{}, [&](int j) {
+      if (j == 0) read_w(st ^ 1, 0, fw[0]);
+      read_x(st ^ 1, j, fx[j]);
+    });
+    read_s(st ^ 1, min(kb + 1, KB - 1));
+    order<FM, 4, 3, 0>();
   }
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no DMA may still write LDS
+  if (KB > 0) {
+#pragma unroll
+    for (int o = FN * FM - kLag; o < FN * FM; ++o) scale_in(o / FM, o % FM, p[o & 3]);
+  }
 
+  // two feature blocks at a time: each token's 64 bytes leave in one store
 #pragma unroll
-  for (int i = 0; i < FN; ++i) {
-    const int n = n0 + wn * WTN + i * 16 + 4 * q4;
-    float bv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (bias && n < N) {
-      const uint2 v = *reinterpret_cast<const uint2*>(bias + n);
-      bv[0] = to_f32<T>((uint16_t)v.x);
-      bv[1] = to_f32<T>((uint16_t)(v.x >> 16));
-      bv[2] = to_f32<T>((uint16_t)v.y);
-      bv[3] = to_f32<T>((uint16_t)(v.y >> 16));
-    }
+  for (int j = 0; j < FM; ++j) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      v4f y = acc[i][j];
+    for (int i = 0; i < FN; i += 2) {
+      const int n = n0 + wn * WTN + i * 16;
+      v4f y[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] += bv[e];
-      store4<T>(y, n, m0 + wm * WTM + j * 16 + r16, M, N, Y);
+      for (int h = 0; h < 2; ++h) {
+        y[h] = acc[i + h][j];
+        const int nh = n + h * 16 + 4 * q4;
+        if (bias && nh < N) {
+          const uint2 v = *reinterpret_cast<const uint2*>(bias + nh);
+          y[h][0] += to_f32<T>((uint16_t)v.x);
+          y[h][1] += to_f32<T>((uint16_t)(v.x >> 16));
+          y[h][2] += to_f32<T>((uint16_t)v.y);
+          y[h][3] += to_f32<T>((uint16_t)(v.y >> 16));
+        }
+      }
+      store32<T>(y[0], y[1], n, m0 + wm * WTM + j * 16, M, N, Y);
     }
   }
 }
 
-template <int T, int BM, int BN, int WM, int WN, int STAGES>
+template <int T, int BM, int BN, int WM, int WN>
 static hipError_t run_gemm(const Fp8Call& c, hipStream_t st) {
+  using L = GemmLds<BM, BN, WM, WN>;
   const int KB = (c.K + kFp8Block - 1) / kFp8Block;
-  constexpr int NBT = BN > 128 ? BN / 128 : 1;
-  constexpr int NWAVE = WM * WN;
-  constexpr int SMEM = STAGES * (BM + BN) * 128 + STAGES * NWAVE * (BM / WM) * 4;
-  static_assert(SMEM + NBT * kMaxKB * 4 <= 160 * 1024, "LDS budget");
-  const int shm = SMEM + (NBT * KB * 4 + 255) / 256 * 256;
+  const int shm = L::SW + (L::NBT * KB * 4 + 255) / 256 * 256;
   const int tilesM = (c.M + BM - 1) / BM, tilesN = (c.N + BN - 1) / BN;
-  auto kern = k_fp8_gemm<T, BM, BN, WM, WN, STAGES>;
+  auto kern = k_fp8_gemm<T, BM, BN, WM, WN>;
   // the dynamic-LDS limit is raised once per device the kernels run on
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   (void)hipGetDevice(&dev);
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_set.load(std::memory_order_relaxed) & bit)) {
-    const hipError_t e =
-        hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize,
-                            SMEM + NBT * kMaxKB * 4);
+    const hipError_t e = hipFuncSetAttribute((const void*)kern,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, L::MAX);
     if (e != hipSuccess) return e;
     attr_set.fetch_or(bit, std::memory_order_relaxed);
   }
-  kern<<<tilesM * tilesN, NWAVE * 64, shm, st>>>(c.X, c.xs, c.W, c.ws, c.bias, c.Y, c.M, c.N, c.K,
-                                                 KB, tilesM, tilesN, tilesM < 4 ? tilesM : 4);
+  kern<<<tilesM * tilesN, WM * WN * 64, shm, st>>>(c.X, c.xs, c.W, c.ws, c.bias, c.Y, c.M, c.N, c.K,
+                                                   KB, tilesM, tilesN, tilesM < 4 ? tilesM : 4);
   return hipGetLastError();
 }
 
 template <int T>
 static hipError_t run_matmul(const Fp8Call& c, hipStream_t st) {
-  return run_gemm<T, 128, 128, 2, 2, 2>(c, st);
+  if ((int64_t)((c.M + 255) / 256) * ((c.N + 255) / 256) >= 256)
+    return run_gemm<T, 256, 256, 4, 2>(c, st);
+  return run_gemm<T, 128, 128, 2, 2>(c, st);
 }
 
 hipError_t launch_fp8_matmul(const Fp8Call& c, hipStream_t st) {
