@@ -34,14 +34,14 @@ constexpr uint32_t kOutOfRange = 0xffffff00u;
 
 // LDS of a tile: two stages of one K block each (W's half blocks, then X's
 // rows), the token scales [stage][wavefront][its tokens], the tile's weight
-// scales [128-feature block][KB].
+// scales [128-feature block][KB + 2].
 template <int BM, int BN, int WM, int WN>
 struct GemmLds {
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int SX = 2 * STAGE;
   static constexpr int SW = SX + 2 * WN * BM * 4;
   static constexpr int NBT = BN > 128 ? BN / 128 : 1;
-  static constexpr int MAX = SW + NBT * kMaxKB * 4;
+  static constexpr int MAX = SW + NBT * (kMaxKB + 2) * 4;
   static_assert(MAX <= 160 * 1024, "LDS budget");
 };
 
@@ -98,10 +98,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   constexpr int NWAVE = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int FM = WTM / 16, FN = WTN / 16;
-  constexpr int WDMA = BN / 8 / NWAVE, XDMA = BM / 8 / NWAVE;  // 1 KB DMAs of a wavefront per stage
-  constexpr int SDMA = WTM / 64;                               // and those of its token scales
-  static_assert(BN / 8 % NWAVE == 0 && BM / 8 % NWAVE == 0 && WTM % 64 == 0, "DMA split");
-  static_assert(128 % WTN == 0 && FN % 2 == 0 && FM >= 4, "a wavefront's features share a scale block");
+  // 1 KB DMAs of a wavefront per K block: of X, of either half of W, and of
+  // its token scales
+  constexpr int XDMA = BM / 8 / NWAVE, HDMA = BN / 16 / NWAVE, SDMA = WTM / 64;
+  static_assert(BN / 16 % NWAVE == 0 && BM / 8 % NWAVE == 0 && WTM % 64 == 0, "DMA split");
+  static_assert(128 % WTN == 0 && FN % 4 == 0 && FM >= 4, "a wavefront's features share a scale block");
   extern __shared__ __align__(16) int8_t smem[];
 
   const int Tt = tilesM * tilesN;
@@ -124,59 +125,75 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   // they only feed outputs that are never stored)
   float* sw = reinterpret_cast<float*>(smem + L::SW);
   const int nbs = (N + kFp8Block - 1) / kFp8Block;
-  for (int i = t; i < L::NBT * KB; i += NWAVE * 64) {
-    const int nb = min(n0 / kFp8Block + i / KB, nbs - 1);
-    sw[i] = ws[(size_t)nb * KB + i % KB];
+  const int KS = KB + 2;  // two zeros behind each block's scales
+  for (int i = t; i < L::NBT * KS; i += NWAVE * 64) {
+    const int nb = min(n0 / kFp8Block + i / KS, nbs - 1), kb = i % KS;
+    sw[i] = kb < KB ? ws[(size_t)nb * KB + kb] : 0.0f;
   }
-  const float* my_sw = sw + (wn * WTN / 128) * KB;
+  const float* my_sw = sw + (wn * WTN / 128) * KS;
 
-  // DMA sources of this wavefront: WDMA half blocks of W and XDMA pieces of 8
-  // rows of X.  Rows past N or M are clamped to the last valid one: they
-  // only feed outputs that are never stored.
+  // DMA sources of this wavefront: XDMA pieces of 8 rows of X, and HDMA half
+  // blocks of either half of W, the first and the second FN / 2 feature
+  // blocks of every wavefront.  Rows past N or M are clamped to the last
+  // valid one: they only feed outputs that are never stored.
   const int xrow = lane >> 3;
   const uint32_t chunk = (lane & 7) ^ xrow;  // the column chunk of this lane's X pieces
-  uint32_t wsrc[WDMA], xsrc[XDMA];
-#pragma unroll
-  for (int j = 0; j < WDMA; ++j) {
-    const int J = w * WDMA + j;
-    const int rb = min(n0 / 16 + J / 2, nrb - 1);
-    wsrc[j] = __builtin_amdgcn_readfirstlane((uint32_t)rb * (uint32_t)KB * 2048u + (J & 1) * 1024u);
-  }
+  uint32_t xsrc[XDMA], wsrc[2][HDMA];
+  int wdst[2][HDMA];
 #pragma unroll
   for (int j = 0; j < XDMA; ++j) {
     const int row = min(m0 + (w * XDMA + j) * 8 + xrow, M - 1);
     xsrc[j] = (uint32_t)row * (uint32_t)K + chunk * 16u;
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < HDMA; ++j) {
+      const int q = w * HDMA + j;  // half block q % 2 of the half's feature block q / 2
+      const int a = q / 2, fb = a / (FN / 2) * FN + a % (FN / 2) + h * (FN / 2);
+      const int rb = min(n0 / 16 + fb, nrb - 1);
+      wsrc[h][j] = __builtin_amdgcn_readfirstlane((uint32_t)rb * (uint32_t)KB * 2048u + (q & 1) * 1024u);
+      wdst[h][j] = __builtin_amdgcn_readfirstlane(fb * 2048 + (q & 1) * 1024);
+    }
   const int mw = min(m0 + wm * WTM, M - 1);
   const uint32_t wbytes = (uint32_t)nrb * (uint32_t)KB * 2048u;
   const uint32_t xbytes = (uint32_t)M * (uint32_t)K;
 
-  // This wavefront's DMAs of K block kb.  Blocks at or past KB get empty
-  // descriptors (zeros), so the loop needs no branch.  In a last block that
-  // K ends inside, chunks at or past K read from an offset out of every
-  // range (zeros); tokens past M read zero scales.
-  constexpr int OPS = WDMA + XDMA + SDMA;
-  auto dma = [&](int kb, int stage, int d0, int d1) {
+  // This wavefront's DMAs of K block kb: `a` takes X, the token scales and
+  // the first half of W, `b` the second half.  Blocks at or past KB get
+  // empty descriptors (zeros), so the loop needs no branch and every
+  // wavefront counts the same number of DMAs.  In a last block that K ends
+  // inside, chunks at or past K read from an offset out of every range
+  // (zeros); tokens past M read zero scales.
+  constexpr int OPA = XDMA + SDMA + HDMA, OPB = HDMA;
+  auto dma_w = [&](int kb, int stage, int h, int j) {
     const bool live = kb < KB;
-    const int k = live ? kb : 0;
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
         (void*)W, (short)0, live ? (int)wbytes : 0, 0x00020000);
+    dma16(rw, smem + stage * L::STAGE + wdst[h][j], lane * 16,
+          (int)(wsrc[h][j] + (uint32_t)(live ? kb : 0) * 2048u));
+  };
+  auto dma_b = [&](int kb, int stage) {
+#pragma unroll
+    for (int j = 0; j < HDMA; ++j) dma_w(kb, stage, 1, j);
+  };
+  auto dma_a = [&](int kb, int stage, int d0, int d1) {
+    const bool live = kb < KB;
+    const int k = live ? kb : 0;
     const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
         (void*)X, (short)0, live ? (int)xbytes : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(xs + (size_t)k * M + mw), (short)0, live ? min(M - mw, WTM) * 4 : 0, 0x00020000);
     const bool out = (uint32_t)k * 128u + chunk * 16u >= (uint32_t)K;
-    int8_t* base = smem + stage * L::STAGE;
 #pragma unroll
     for (int d = d0; d < d1; ++d) {
-      if (d < WDMA) {
-        dma16(rw, base + (w * WDMA + d) * 1024, lane * 16, (int)(wsrc[d] + (uint32_t)k * 2048u));
-      } else if (d < WDMA + XDMA) {
-        const int j = d - WDMA;
-        dma16(rx, base + BN * 128 + (w * XDMA + j) * 1024, (int)(out ? kOutOfRange : xsrc[j]),
-              k * 128);
+      if (d < XDMA) {
+        dma16(rx, smem + stage * L::STAGE + BN * 128 + (w * XDMA + d) * 1024,
+              (int)(out ? kOutOfRange : xsrc[d]), k * 128);
+      } else if (d < XDMA + HDMA) {
+        dma_w(kb, stage, 0, d - XDMA);
       } else {
-        const int j = d - WDMA - XDMA;
+        const int j = d - XDMA - HDMA;
         dma4(rs, smem + L::SX + ((stage * NWAVE + w) * WTM + j * 64) * 4, lane * 4 + j * 256, 0);
       }
     }
@@ -197,25 +214,34 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   float sx[FM], s[FM] = {};
   float s_w = 0.0f;
   v4f p[4] = {};
-  const int8_t* wb = smem + (wn * WTN / 16) * 2048 + lane * 16;
-  const int8_t* xb = smem + BN * 128 + (wm * WTM + r16) * 128;
-  const int xlo = (q4 ^ (r16 & 7)) * 16, xhi = ((q4 + 4) ^ (r16 & 7)) * 16;
+  // LDS offsets of the lane's fragments and scales in either stage.  The
+  // empty asm hides that one is the other plus a constant: as immediate
+  // offsets of the reads the constants do not fit, and would be added anew
+  // in front of each.
+  int wo[2], xlo[2], xhi[2];
+#pragma unroll
+  for (int st = 0; st < 2; ++st) {
+    wo[st] = st * L::STAGE + (wn * WTN / 16) * 2048 + lane * 16;
+    const int xo = st * L::STAGE + BN * 128 + (wm * WTM + r16) * 128;
+    xlo[st] = xo + (q4 ^ (r16 & 7)) * 16;
+    xhi[st] = xo + ((q4 + 4) ^ (r16 & 7)) * 16;
+    asm volatile("" : "+v"(wo[st]), "+v"(xlo[st]), "+v"(xhi[st]));
+  }
+  const float* sbase = reinterpret_cast<const float*>(smem + L::SX) + w * WTM + r16;
+  auto join = [](const v4i& lo, const v4i& hi) {
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
   auto read_w = [&](int stage, int i, v8i& f) {
-    const int8_t* q = wb + stage * L::STAGE + i * 2048;
-    const v4i lo = *reinterpret_cast<const v4i*>(q);
-    const v4i hi = *reinterpret_cast<const v4i*>(q + 1024);
-    f = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    const int8_t* q = smem + wo[stage] + i * 2048;
+    f = join(*reinterpret_cast<const v4i*>(q), *reinterpret_cast<const v4i*>(q + 1024));
   };
   auto read_x = [&](int stage, int j, v8i& f) {
-    const int8_t* q = xb + stage * L::STAGE + j * 2048;
-    const v4i lo = *reinterpret_cast<const v4i*>(q + xlo);
-    const v4i hi = *reinterpret_cast<const v4i*>(q + xhi);
-    f = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    f = join(*reinterpret_cast<const v4i*>(smem + xlo[stage] + j * 2048),
+             *reinterpret_cast<const v4i*>(smem + xhi[stage] + j * 2048));
   };
   auto read_s = [&](int stage, int kb) {
-    const float* q = reinterpret_cast<const float*>(smem + L::SX) + (stage * NWAVE + w) * WTM + r16;
 #pragma unroll
-    for (int j = 0; j < FM; ++j) sx[j] = q[j * 16];
+    for (int j = 0; j < FM; ++j) sx[j] = sbase[stage * NWAVE * WTM + j * 16];
     s_w = my_sw[kb];
   };
   auto scale_in = [&](int i, int j, const v4f& v) {
@@ -224,15 +250,17 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   };
 
   if (KB > 0) {
-    dma(0, 0, 0, OPS);
-    __syncthreads();  // the weight scales and the first stage
+    dma_a(0, 0, 0, OPA);
+    dma_b(0, 0);
+    dma_a(1, 1, 0, OPA);
+    barrier_vm<OPA + OPB>();  // the weight scales, and the first DMAs of block 0
     read_s(0, 0);
 #pragma unroll
     for (int j = 0; j < FM; ++j) read_x(0, j, fx[j]);
     read_w(0, 0, fw[0]);
   }
-  for (int kb = 0; kb < KB; ++kb) {
-    const int st = kb & 1;
+  auto step = [&](auto ST, int kb) {
+    constexpr int st = decltype(ST)::value;
     // feature block i of K block kb; `with(j)` issues loads after MFMA j
     auto group = [&](auto I, auto&& with) {
       constexpr int i = decltype(I)::value;
@@ -250,27 +278,46 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     };
     auto upto = [&](auto I) {
       constexpr int i = decltype(I)::value;
-      // K block kb + 1 goes into the other stage, free since the last
-      // barrier, its DMAs spread over the first two feature blocks
-      constexpr int v0 = i == 0 ? 0 : (OPS + 1) / 2, v1 = i == 0 ? (OPS + 1) / 2 : OPS;
+      constexpr int A = FN / 2 - 1;  // first feature block after the first barrier
+      // the DMAs a barrier has made room for, spread over feature blocks
+      constexpr int a0 = i == A ? 0 : i == A + 1 ? (OPA + 1) / 2 : OPA;
+      constexpr int a1 = i == A ? (OPA + 1) / 2 : OPA;
+      constexpr int V = i == 0 ? OPB : i >= A ? a1 - a0 : 0;
+      static_assert(A > 0, "");
       group(I, [&](int j) {
         if (j == 0) read_w(st, i + 1, fw[(i + 1) & 1]);
       });
-      if constexpr (i < 2) dma(kb + 1, st ^ 1, v0, v1);
-      order<FM, 2, 0, i < 2 ? v1 - v0 : 0>();
+      if constexpr (i == 0) dma_b(kb + 1, st ^ 1);
+      if constexpr (i == A || i == A + 1) dma_a(kb + 2, st, a0, a1);
+      order<FM, 2, 0, V>();
+      if constexpr (i == A - 1) {
+        // every wavefront has read X and the first half of W of this K block,
+        // and its DMAs of the second half have landed (issued 1.5 K blocks
+        // ago; since then the A part of kb + 1 and the B part of kb + 1)
+        barrier_vm<OPA + OPB>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
     };
     unroll(upto, std::make_integer_sequence<int, FN - 1>{});
-    // every wavefront has read all of K block kb's stage, and its own DMAs of
-    // kb + 1 have landed: that stage may be overwritten, the other be read
-    barrier_vm<0>();
+    // every wavefront has read the second half of W, and its DMAs of the next
+    // K block's X and first half of W have landed (since then issued: the B
+    // part of kb + 1 and the A part of kb + 2)
+    barrier_vm<OPA + OPB>();
     __builtin_amdgcn_sched_barrier(0);
     group(std::integral_constant<int, FN - 1>{}, [&](int j) {
       if (j == 0) read_w(st ^ 1, 0, fw[0]);
       read_x(st ^ 1, j, fx[j]);
     });
-    read_s(st ^ 1, min(kb + 1, KB - 1));
+    read_s(st ^ 1, kb + 1);
     order<FM, 4, 3, 0>();
+  };
+  // two K blocks per iteration, so that the stage is a constant in each; an
+  // odd KB ends with a block of zero operands and zero scales
+  for (int kb = 0; kb < KB; kb += 2) {
+    step(std::integral_constant<int, 0>{}, kb);
+    step(std::integral_constant<int, 1>{}, kb + 1);
   }
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no DMA may still write LDS
   if (KB > 0) {
 #pragma unroll
     for (int o = FN * FM - kLag; o < FN * FM; ++o) scale_in(o / FM, o % FM, p[o & 3]);
@@ -304,7 +351,7 @@ template <int T, int BM, int BN, int WM, int WN>
 static hipError_t run_gemm(const Fp8Call& c, hipStream_t st) {
   using L = GemmLds<BM, BN, WM, WN>;
   const int KB = (c.K + kFp8Block - 1) / kFp8Block;
-  const int shm = L::SW + (L::NBT * KB * 4 + 255) / 256 * 256;
+  const int shm = L::SW + L::NBT * (KB + 2) * 4;
   const int tilesM = (c.M + BM - 1) / BM, tilesN = (c.N + BN - 1) / BN;
   auto kern = k_fp8_gemm<T, BM, BN, WM, WN>;
   // the dynamic-LDS limit is raised once per device the kernels run on
