@@ -34,12 +34,13 @@ constexpr uint32_t kOutOfRange = 0xffffff00u;
 
 // LDS of a tile: two stages of one K block each (W's half blocks, then X's
 // rows), the token scales [stage][wavefront][its tokens], the tile's weight
-// scales [128-feature block][KB + 2].
+// scales [128-feature block][KB + 2], and its bias in fp32.
 template <int BM, int BN, int WM, int WN>
 struct GemmLds {
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int SX = 2 * STAGE;
-  static constexpr int SW = SX + 2 * WN * BM * 4;
+  static constexpr int SB = SX + 2 * WN * BM * 4;
+  static constexpr int SW = SB + BN * 4;
   static constexpr int NBT = BN > 128 ? BN / 128 : 1;
   static constexpr int MAX = SW + NBT * (kMaxKB + 2) * 4;
   static_assert(MAX <= 160 * 1024, "LDS budget");
@@ -122,14 +123,19 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   const int q4 = lane >> 4, r16 = lane & 15;
 
   // the tile's weight scales (blocks past the last 128 features repeat it:
-  // they only feed outputs that are never stored)
+  // they only feed outputs that are never stored) and its bias; the loads of
+  // the first round are in flight under the first DMAs
   float* sw = reinterpret_cast<float*>(smem + L::SW);
+  float* sb = reinterpret_cast<float*>(smem + L::SB);
   const int nbs = (N + kFp8Block - 1) / kFp8Block;
   const int KS = KB + 2;  // two zeros behind each block's scales
-  for (int i = t; i < L::NBT * KS; i += NWAVE * 64) {
+  auto weight_scale = [&](int i) {
     const int nb = min(n0 / kFp8Block + i / KS, nbs - 1), kb = i % KS;
-    sw[i] = kb < KB ? ws[(size_t)nb * KB + kb] : 0.0f;
-  }
+    return kb < KB ? ws[(size_t)nb * KB + kb] : 0.0f;
+  };
+  const float sw_first = t < L::NBT * KS ? weight_scale(t) : 0.0f;
+  const uint16_t bias_first = bias && t < BN && n0 + t < N ? bias[n0 + t] : (uint16_t)0;
+  static_assert(BN <= NWAVE * 64, "one bias value per thread");
   const float* my_sw = sw + (wn * WTN / 128) * KS;
 
   // DMA sources of this wavefront: XDMA pieces of 8 rows of X, and HDMA half
@@ -173,9 +179,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     dma16(rw, smem + stage * L::STAGE + wdst[h][j], lane * 16,
           (int)(wsrc[h][j] + (uint32_t)(live ? kb : 0) * 2048u));
   };
-  auto dma_b = [&](int kb, int stage) {
+  auto dma_b = [&](int kb, int stage, int d0, int d1) {
 #pragma unroll
-    for (int j = 0; j < HDMA; ++j) dma_w(kb, stage, 1, j);
+    for (int d = d0; d < d1; ++d) dma_w(kb, stage, 1, d);
   };
   auto dma_a = [&](int kb, int stage, int d0, int d1) {
     const bool live = kb < KB;
@@ -251,8 +257,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
 
   if (KB > 0) {
     dma_a(0, 0, 0, OPA);
-    dma_b(0, 0);
+    dma_b(0, 0, 0, OPB);
     dma_a(1, 1, 0, OPA);
+  }
+  if (t < BN) sb[t] = to_f32<T>(bias_first);
+  if (KB > 0) {
+    for (int i = t; i < L::NBT * KS; i += NWAVE * 64) sw[i] = i == t ? sw_first : weight_scale(i);
     barrier_vm<OPA + OPB>();  // the weight scales, and the first DMAs of block 0
     read_s(0, 0);
 #pragma unroll
@@ -279,17 +289,19 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     auto upto = [&](auto I) {
       constexpr int i = decltype(I)::value;
       constexpr int A = FN / 2 - 1;  // first feature block after the first barrier
-      // the DMAs a barrier has made room for, spread over feature blocks
-      constexpr int a0 = i == A ? 0 : i == A + 1 ? (OPA + 1) / 2 : OPA;
-      constexpr int a1 = i == A ? (OPA + 1) / 2 : OPA;
-      constexpr int V = i == 0 ? OPB : i >= A ? a1 - a0 : 0;
+      // the DMAs a barrier has made room for, spread over the feature blocks
+      // up to the other barrier: a burst fills the address unit's queue and
+      // holds up the MFMAs behind it
+      constexpr int a0 = i < A ? 0 : (i - A) * OPA / (FN - 1 - A);
+      constexpr int a1 = i < A ? 0 : (i + 1 - A) * OPA / (FN - 1 - A);
+      constexpr int b0 = i < A ? i * OPB / A : 0, b1 = i < A ? (i + 1) * OPB / A : 0;
       static_assert(A > 0, "");
       group(I, [&](int j) {
         if (j == 0) read_w(st, i + 1, fw[(i + 1) & 1]);
       });
-      if constexpr (i == 0) dma_b(kb + 1, st ^ 1);
-      if constexpr (i == A || i == A + 1) dma_a(kb + 2, st, a0, a1);
-      order<FM, 2, 0, V>();
+      dma_a(kb + 2, st, a0, a1);
+      dma_b(kb + 1, st ^ 1, b0, b1);
+      order<FM, 2, 0, a1 - a0 + b1 - b0>();
       if constexpr (i == A - 1) {
         // every wavefront has read X and the first half of W of this K block,
         // and its DMAs of the second half have landed (issued 1.5 K blocks
@@ -318,6 +330,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     step(std::integral_constant<int, 1>{}, kb + 1);
   }
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no DMA may still write LDS
+  if (KB == 0) __syncthreads();              // the bias
   if (KB > 0) {
 #pragma unroll
     for (int o = FN * FM - kLag; o < FN * FM; ++o) scale_in(o / FM, o % FM, p[o & 3]);
@@ -325,25 +338,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
 
   // two feature blocks at a time: each token's 64 bytes leave in one store
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
+  for (int i = 0; i < FN; i += 2) {
+    const int nl = wn * WTN + i * 16;
+    const v4f ba = *reinterpret_cast<const v4f*>(sb + nl + 4 * q4);
+    const v4f bb = *reinterpret_cast<const v4f*>(sb + nl + 16 + 4 * q4);
 #pragma unroll
-    for (int i = 0; i < FN; i += 2) {
-      const int n = n0 + wn * WTN + i * 16;
-      v4f y[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        y[h] = acc[i + h][j];
-        const int nh = n + h * 16 + 4 * q4;
-        if (bias && nh < N) {
-          const uint2 v = *reinterpret_cast<const uint2*>(bias + nh);
-          y[h][0] += to_f32<T>((uint16_t)v.x);
-          y[h][1] += to_f32<T>((uint16_t)(v.x >> 16));
-          y[h][2] += to_f32<T>((uint16_t)v.y);
-          y[h][3] += to_f32<T>((uint16_t)(v.y >> 16));
-        }
-      }
-      store32<T>(y[0], y[1], n, m0 + wm * WTM + j * 16, M, N, Y);
-    }
+    for (int j = 0; j < FM; ++j)
+      store32<T>(acc[i][j] + ba, acc[i + 1][j] + bb, n0 + nl, m0 + wm * WTM + j * 16, M, N, Y);
   }
 }
 
