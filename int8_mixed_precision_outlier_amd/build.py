@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libint8mm.so")
 SOURCES = ["prologue.hip", "gemm.hip", "decode.hip", "noalloc.hip", "api.cpp",
-           "fp8_rows.hip", "fp8_gemm.hip", "fp8_api.cpp"]
+           "fp8_rows.hip", "fp8_gemm.hip", "fp8_decode.hip", "fp8_api.cpp"]
 # the peak probes (include/int8mm_probes.h): measurement only, own library
 PROBE_LIB = os.path.join(PKG, "libint8mm_probes.so")
 PROBE_SOURCES = ["probes.hip"]

@@ -24,6 +24,8 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 constexpr int kFp8Block = 128;        // columns (and features) per scale
 constexpr float kE4m3Max = 448.0f;    // largest e4m3 magnitude
 constexpr float kScaleFloor = 0x1p-100f;
+// A buffer offset past every operand (they hold at most 2^31 bytes).
+constexpr uint32_t kOutOfRange = 0xffffff00u;
 
 // The 16-bit types: kF16 / kBf16 name them in template arguments.
 constexpr int kF16 = 0, kBf16 = 1;
@@ -114,6 +116,17 @@ struct Fp8Call {
   uint16_t* Y;
   int M, N, K, type;
 };
+
+// The launches of an M x N x K product: features [0, n1) in tiles `first`,
+// [n1, N) (if any) in tiles `second`.
+enum { kTile256 = 0, kTile256x128 = 1, kTile128 = 2 };
+struct Fp8Plan {
+  int first, n1, second;
+};
+Fp8Plan fp8_plan(int M, int N);
+// The product for at most kFp8DecodeMaxM tokens.
+constexpr int kFp8DecodeMaxM = 64;
+hipError_t launch_fp8_decode(const Fp8Call& c, hipStream_t st);
 hipError_t launch_fp8_matmul(const Fp8Call& c, hipStream_t st);
 
 }  // namespace i8mm

@@ -1,0 +1,238 @@
+// Block-scaled e4m3 product for few tokens (gfx950): the packed weight is
+// streamed from HBM exactly once, every byte feeding a 16x16x128 e4m3 MFMA
+// whose 16 columns are tokens.
+//
+// A workgroup owns R blocks of 16 features over all of K, so nothing is
+// combined across workgroups; its KS wavefronts take the K blocks in turn, U
+// at a time, and add their partial sums through LDS at the end in a fixed
+// order.  A wavefront's K block of 16 features is 2 KB of contiguous W, two
+// 16-byte loads per lane in exactly the MFMA's operand layout (nontemporal:
+// the stream is never read again).  The tokens' bytes and scales reach a part
+// of LDS that is the wavefront's own, by DMA, so no barrier is needed: an
+// instruction moves 8 rows x 128 bytes, whole cache lines, with the chunks of
+// a row swapped as in fp8_gemm.hip, where 16 rows x 64 bytes straight into
+// registers fetched each line twice (a CU then took in 38 GB/s, too little
+// for HBM's rate at more than 16 tokens: 32x20480x5120 33.6 us).  The next U K
+// blocks are on their way under the MFMAs and scaling fmas of the current ones.
+//
+// Bound by HBM: at 64 tokens the product does 128 operations per weight byte.
+#include "common.hpp"
+#include "fp8.hpp"
+
+#include <atomic>
+
+namespace i8mm {
+
+// Waits until at most VM of this wavefront's vector-memory operations are
+// outstanding; no memory access moves across.
+template <int VM>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(VM < 64, "waitcnt field");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(VM));
+  asm volatile("" ::: "memory");
+}
+
+// LDS: two stages of U K blocks per wavefront, each T x 16 rows of 128 bytes
+// and 64 token scales; at the end the partial sums.
+template <int R, int T, int KS, int U>
+struct DecodeLds {
+  static constexpr int BLOCK = T * 2048 + 256;
+  static constexpr int WAVE = 2 * U * BLOCK;
+  static constexpr int SUMS = KS * R * T * 1024;
+  static constexpr int SIZE = KS * WAVE > SUMS ? KS * WAVE : SUMS;
+  static_assert(SIZE <= 160 * 1024, "LDS budget");
+};
+
+template <int TY, int R, int T, int KS, int U>
+__global__ __launch_bounds__(KS * 64) void k_fp8_decode(
+    const uint8_t* __restrict__ X, const float* __restrict__ xs, const uint8_t* __restrict__ W,
+    const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y, int M, int N, int K, int KB) {
+  using L = DecodeLds<R, T, KS, U>;
+  extern __shared__ __align__(16) int8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q4 = lane >> 4, r16 = lane & 15;
+  const int nrb = N >> 4;
+  const int rb0 = blockIdx.x * R;
+  int8_t* mine = smem + w * L::WAVE;
+
+  // rows past M and features past N repeat the last one: they only feed
+  // outputs that are never stored
+  const int xrow = lane >> 3;
+  const uint32_t chunk = (lane & 7) ^ xrow;
+  uint32_t xsrc[2 * T];
+#pragma unroll
+  for (int t = 0; t < 2 * T; ++t)
+    xsrc[t] = (uint32_t)min(t * 8 + xrow, M - 1) * (uint32_t)K + chunk * 16u;
+  uint32_t wsrc[R];
+  // the weight scales through the constant address space: scalar loads
+  typedef const __attribute__((address_space(4))) float* scalar_ptr;
+  scalar_ptr wsrow[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int rb = min(rb0 + r, nrb - 1);
+    wsrc[r] = (uint32_t)rb * (uint32_t)KB * 2048u;
+    wsrow[r] = (scalar_ptr)(uintptr_t)(ws + (size_t)(rb / 8) * KB);
+  }
+  const uint32_t xbytes = (uint32_t)M * (uint32_t)K;
+  const uint32_t wbytes = (uint32_t)nrb * (uint32_t)KB * 2048u;
+
+  struct Weights {
+    v4i w[U][R][2];
+    float s[U][R];
+  };
+  // Loads of K blocks kb .. kb + U - 1 into registers and a stage of LDS.
+  // Blocks at or past KB get empty descriptors and zero scales, and the
+  // columns at or past K of a last block that K ends inside are read from an
+  // offset out of every range: zeros.  So a load has no branch and always the
+  // same OPS vector loads, which the wait in `step` counts.
+  constexpr int OPS = U * (2 * T + 1 + 2 * R);
+  constexpr int kNonTemporal = 2;
+  auto load = [&](int kb, int stage, Weights& o) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool live = kb + u < KB;
+      const int k = live ? kb + u : 0;
+      const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)X, (short)0, live ? (int)xbytes : 0, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(xs + (size_t)k * M), (short)0, live ? M * 4 : 0, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)W, (short)0, live ? (int)wbytes : 0, 0x00020000);
+      const bool out = (uint32_t)k * 128u + chunk * 16u >= (uint32_t)K;
+      int8_t* dst = mine + (stage * U + u) * L::BLOCK;
+#pragma unroll
+      for (int t = 0; t < 2 * T; ++t)
+        dma16(rx, dst + t * 1024, (int)(out ? kOutOfRange : xsrc[t]), k * 128);
+      dma4(rs, dst + T * 2048, lane * 4, 0);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        o.s[u][r] = wsrow[r][k];  // block 0's past KB; `compute` takes zero there
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          o.w[u][r][h] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                       rw, lane * 16, (int)(wsrc[r] + (uint32_t)k * 2048u + h * 1024u), kNonTemporal));
+      }
+    }
+  };
+
+  v4f acc[R][T];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[r][t] = v4f{};
+  auto join = [](const v4i& lo, const v4i& hi) {
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto compute = [&](int kb, int stage, const Weights& o) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool live = kb + u < KB;
+      const int8_t* src = mine + (stage * U + u) * L::BLOCK;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const int8_t* row = src + (t * 16 + r16) * 128;
+        const v8i x = join(*reinterpret_cast<const v4i*>(row + (q4 ^ (r16 & 7)) * 16),
+                           *reinterpret_cast<const v4i*>(row + ((q4 + 4) ^ (r16 & 7)) * 16));
+        const float sx = *reinterpret_cast<const float*>(src + T * 2048 + (t * 16 + r16) * 4);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float s = sx * (live ? o.s[u][r] : 0.0f);
+          const v4f p = mfma16_e4m3(join(o.w[u][r][0], o.w[u][r][1]), x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[r][t][e] = fmaf(p[e], s, acc[r][t][e]);
+        }
+      }
+    }
+  };
+  // a step: the next K blocks' loads, then the wait for the current ones'
+  auto step = [&](int kb, int stage, const Weights& cur, Weights& next) {
+    load(kb + KS * U, stage ^ 1, next);
+    wait_vm<OPS>();
+    compute(kb, stage, cur);
+    // the stage's reads are done before the next step's DMAs overwrite it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+
+  Weights a, b;
+  if (w * U < KB) {
+    load(w * U, 0, a);
+    for (int kb = w * U; kb < KB; kb += 2 * KS * U) {
+      step(kb, 0, a, b);
+      step(kb + KS * U, 1, b, a);
+    }
+  }
+  wait_vm<0>();  // no DMA may still write LDS
+  __syncthreads();  // the partial sums overwrite the stages
+  v4f(*red)[R * T][64] = reinterpret_cast<v4f(*)[R * T][64]>(smem);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t) red[w][r * T + t][lane] = acc[r][t];
+  __syncthreads();
+  // the R * T blocks of 16 features x 16 tokens over the wavefronts: the
+  // partial sums in wavefront order, the bias, one store of 4 features
+  for (int o = w; o < R * T; o += KS) {
+    v4f y = red[0][o][lane];
+#pragma unroll
+    for (int i = 1; i < KS; ++i) y += red[i][o][lane];
+    const int n = (rb0 + o / T) * 16 + 4 * q4, m = o % T * 16 + r16;
+    if (m < M && n < N) {
+      if (bias) {
+        const uint2 v = *reinterpret_cast<const uint2*>(bias + n);
+        y[0] += to_f32<TY>((uint16_t)v.x);
+        y[1] += to_f32<TY>((uint16_t)(v.x >> 16));
+        y[2] += to_f32<TY>((uint16_t)v.y);
+        y[3] += to_f32<TY>((uint16_t)(v.y >> 16));
+      }
+      *reinterpret_cast<uint2*>(Y + (size_t)m * N + n) =
+          make_uint2(pack16x2<TY>(y[0], y[1]), pack16x2<TY>(y[2], y[3]));
+    }
+  }
+}
+
+template <int TY, int R, int T, int KS, int U>
+static hipError_t run_decode(const Fp8Call& c, hipStream_t st) {
+  constexpr int SMEM = DecodeLds<R, T, KS, U>::SIZE;
+  auto kern = k_fp8_decode<TY, R, T, KS, U>;
+  // the dynamic-LDS limit is raised once per device the kernels run on
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  (void)hipGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_set.load(std::memory_order_relaxed) & bit)) {
+    const hipError_t e = hipFuncSetAttribute((const void*)kern,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != hipSuccess) return e;
+    attr_set.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int KB = (c.K + kFp8Block - 1) / kFp8Block;
+  kern<<<(c.N / 16 + R - 1) / R, KS * 64, SMEM, st>>>(c.X, c.xs, c.W, c.ws, c.bias, c.Y, c.M, c.N,
+                                                      c.K, KB);
+  return hipGetLastError();
+}
+
+#ifndef DR
+#define DR 1
+#define DKS 8
+#define DU 1
+#endif
+
+template <int TY>
+static hipError_t decode_tokens(const Fp8Call& c, hipStream_t st) {
+  switch ((c.M + 15) / 16) {
+    case 1: return run_decode<TY, DR, 1, DKS, DU>(c, st);
+    case 2: return run_decode<TY, DR, 2, DKS, DU>(c, st);
+    case 3: return run_decode<TY, DR, 3, DKS, DU>(c, st);
+    default: return run_decode<TY, DR, 4, DKS, DU>(c, st);
+  }
+}
+
+hipError_t launch_fp8_decode(const Fp8Call& c, hipStream_t st) {
+  return c.type == kF16 ? decode_tokens<kF16>(c, st) : decode_tokens<kBf16>(c, st);
+}
+
+}  // namespace i8mm

@@ -20,6 +20,7 @@
 // weight's scales of the tile are staged once.
 #include "common.hpp"
 #include "fp8.hpp"
+#include "launch.hpp"
 
 #include <atomic>
 #include <utility>
@@ -29,8 +30,6 @@ namespace i8mm {
 namespace {
 
 constexpr int kMaxKB = 65536 / kFp8Block;
-// A buffer offset past every operand (they hold at most 2^31 bytes).
-constexpr uint32_t kOutOfRange = 0xffffff00u;
 
 // LDS of a tile: two stages of one K block each (W's half blocks, then X's
 // rows), the token scales [stage][wavefront][its tokens], the tile's weight
@@ -94,7 +93,7 @@ template <int T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     const uint8_t* __restrict__ X, const float* __restrict__ xs, const uint8_t* __restrict__ W,
     const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y,
-    int M, int N, int K, int KB, int tilesM, int tilesN, int groupM) {
+    int M, int N, int K, int KB, int tilesM, int tilesN, int groupM, int nbase) {
   using L = GemmLds<BM, BN, WM, WN>;
   constexpr int NWAVE = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
@@ -114,7 +113,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   const int gsz = min(tilesM - first_m, groupM);
   const int tm = first_m + (b % per_group) % gsz;
   const int tn = (b % per_group) / gsz;
-  const int m0 = tm * BM, n0 = tn * BN;
+  // the launch covers the features from nbase on, tilesN tiles of BN
+  const int m0 = tm * BM, n0 = nbase + tn * BN;
 
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -348,12 +348,14 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   }
 }
 
+// One launch over the features [nbase, nend); nend is N, or a multiple of BN
+// above nbase.
 template <int T, int BM, int BN, int WM, int WN>
-static hipError_t run_gemm(const Fp8Call& c, hipStream_t st) {
+static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st) {
   using L = GemmLds<BM, BN, WM, WN>;
   const int KB = (c.K + kFp8Block - 1) / kFp8Block;
   const int shm = L::SW + L::NBT * (KB + 2) * 4;
-  const int tilesM = (c.M + BM - 1) / BM, tilesN = (c.N + BN - 1) / BN;
+  const int tilesM = (c.M + BM - 1) / BM, tilesN = (nend - nbase + BN - 1) / BN;
   auto kern = k_fp8_gemm<T, BM, BN, WM, WN>;
   // the dynamic-LDS limit is raised once per device the kernels run on
   static std::atomic<uint64_t> attr_set{0};
@@ -366,19 +368,89 @@ static hipError_t run_gemm(const Fp8Call& c, hipStream_t st) {
     if (e != hipSuccess) return e;
     attr_set.fetch_or(bit, std::memory_order_relaxed);
   }
+  // groups of 4 token tiles: the 32 tiles an XCD runs at once share 4 token
+  // and 8 feature panels in its L2 (4096x12288x49152: 1963 us; 2 tiles 2035,
+  // 8 tiles 1975, 16 tiles 2040)
   kern<<<tilesM * tilesN, WM * WN * 64, shm, st>>>(c.X, c.xs, c.W, c.ws, c.bias, c.Y, c.M, c.N, c.K,
-                                                   KB, tilesM, tilesN, tilesM < 4 ? tilesM : 4);
+                                                   KB, tilesM, tilesN, tilesM < 4 ? tilesM : 4, nbase);
   return hipGetLastError();
 }
 
 template <int T>
+static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipStream_t st) {
+  switch (cfg) {
+    case kTile128: return run_gemm<T, 128, 128, 2, 2>(c, nbase, nend, st);
+    case kTile256x128: return run_gemm<T, 256, 128, 4, 2>(c, nbase, nend, st);
+    default: return run_gemm<T, 256, 256, 4, 2>(c, nbase, nend, st);
+  }
+}
+
+// Tile configuration.  The cost of a launch is counted in rounds of
+// workgroups over the chip, in units of a round of 256x256 tiles (8
+// wavefronts of 64 tokens x 128 features, one workgroup per CU), fitted at
+// K = 4096 and 5120 (us; 256x256 / 256x128 / 128x128 tiles):
+//   256x128  0.70 per round (one workgroup per CU; 2048x4096x4096: 49.4 /
+//            36.6 / 37.5);
+//   128x128  0.76 per round of two workgroups per CU, 0.42 for a last round
+//            of at most one per CU (512x5120x5120: 52.9 / 35.3 / 26.3,
+//            512x5120x20480: 62.5 / 83.4 / 75.0).
+// When 256x256 tiles would leave the last round partly empty, the features
+// can be split: [0, n1) in whole rounds of 256x256 tiles, [n1, N) in a second
+// launch of smaller tiles (kGap for its fill and drain, taken when it saves
+// more than kMargin).
+constexpr double kF128 = 0.76, kF128Half = 0.42, kF256x128 = 0.70, kGap = 0.04, kMargin = 0.05;
+
+static double tile_cost(int cfg, long M, long N, long cus) {
+  if (cfg == kTile128) {
+    const long t = (M + 127) / 128 * ((N + 127) / 128), rest = t % (2 * cus);
+    return kF128 * (double)(t / (2 * cus)) + (rest == 0 ? 0.0 : rest <= cus ? kF128Half : kF128);
+  }
+  const long bn = cfg == kTile256 ? 256 : 128;
+  const long t = (M + 255) / 256 * ((N + bn - 1) / bn);
+  return (cfg == kTile256 ? 1.0 : kF256x128) * (double)((t + cus - 1) / cus);
+}
+
+Fp8Plan fp8_plan(int M, int N) {
+  const long cus = device_cu_count();
+  auto cheapest = [&](long n, double* cost) {  // ties keep the larger tile
+    int best = kTile256;
+    *cost = tile_cost(kTile256, M, n, cus);
+    for (int c : {kTile256x128, kTile128}) {
+      const double v = tile_cost(c, M, n, cus);
+      if (v < *cost) {
+        best = c;
+        *cost = v;
+      }
+    }
+    return best;
+  };
+  double cbest;
+  Fp8Plan best{cheapest(N, &cbest), N, 0};
+  const long tm = (M + 255) / 256, t256 = tm * ((N + 255) / 256);
+  for (long R = 1; R * cus < t256; ++R) {
+    const long n1 = R * cus / tm * 256;
+    if (n1 <= 0 || n1 >= N) continue;
+    double rest;
+    const int second = cheapest(N - n1, &rest);
+    const double c = tile_cost(kTile256, M, n1, cus) + kGap + rest;
+    if (second != kTile256 && c < cbest - kMargin) {
+      best = Fp8Plan{kTile256, (int)n1, second};
+      cbest = c;
+    }
+  }
+  return best;
+}
+
+template <int T>
 static hipError_t run_matmul(const Fp8Call& c, hipStream_t st) {
-  if ((int64_t)((c.M + 255) / 256) * ((c.N + 255) / 256) >= 256)
-    return run_gemm<T, 256, 256, 4, 2>(c, st);
-  return run_gemm<T, 128, 128, 2, 2>(c, st);
+  const Fp8Plan p = fp8_plan(c.M, c.N);
+  const hipError_t e = run_tiles<T>(p.first, c, 0, p.n1, st);
+  if (e != hipSuccess || p.n1 >= c.N) return e;
+  return run_tiles<T>(p.second, c, p.n1, c.N, st);
 }
 
 hipError_t launch_fp8_matmul(const Fp8Call& c, hipStream_t st) {
+  if (c.M <= kFp8DecodeMaxM) return launch_fp8_decode(c, st);
   return c.type == kF16 ? run_matmul<kF16>(c, st) : run_matmul<kBf16>(c, st);
 }
 
