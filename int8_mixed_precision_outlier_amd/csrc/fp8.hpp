@@ -117,15 +117,20 @@ struct Fp8Call {
   int M, N, K, type;
 };
 
-// The launches of an M x N x K product: features [0, n1) in tiles `first`,
-// [n1, N) (if any) in tiles `second`.
-enum { kTile256 = 0, kTile256x128 = 1, kTile128 = 2 };
+// The kernels of an M x N product.  Tiles: features [0, n1) in tiles `first`,
+// [n1, N) (if any) in tiles `second`; kDecode: the weight-streaming kernel
+// with R feature and T token blocks of 16.
+enum { kDecode = -1, kTile256 = 0, kTile256x128 = 1, kTile128 = 2, kTile128Deep = 3 };
 struct Fp8Plan {
   int first, n1, second;
 };
 Fp8Plan fp8_plan(int M, int N);
-// The product for at most kFp8DecodeMaxM tokens.
-constexpr int kFp8DecodeMaxM = 64;
+constexpr int kFp8DecodeMaxM = 128;
+struct Fp8DecodePlan {
+  int R, T;
+  int64_t cost;  // rounds of workgroups * (R + T)
+};
+Fp8DecodePlan fp8_decode_plan(int M, int N);  // M <= kFp8DecodeMaxM
 hipError_t launch_fp8_decode(const Fp8Call& c, hipStream_t st);
 hipError_t launch_fp8_matmul(const Fp8Call& c, hipStream_t st);
 

@@ -1,4 +1,4 @@
-// Block-scaled e4m3 product for few tokens (gfx950): the packed weight is
+// Block-scaled e4m3 product for few tokens, at most 128 (gfx950): the packed weight is
 // streamed from HBM exactly once, every byte feeding a 16x16x128 e4m3 MFMA
 // whose 16 columns are tokens.
 //
@@ -15,9 +15,12 @@
 // for HBM's rate at more than 16 tokens: 32x20480x5120 33.6 us).  The next U K
 // blocks are on their way under the MFMAs and scaling fmas of the current ones.
 //
-// Bound by HBM: at 64 tokens the product does 128 operations per weight byte.
+// Bound by HBM for a few tokens (1x12288x49152: 86 us = 7.0 TB/s, 32x12288x36864:
+// 71 us = 6.4 TB/s), by what a CU takes in of both operands (about 55 GB/s)
+// towards 128.
 #include "common.hpp"
 #include "fp8.hpp"
+#include "launch.hpp"
 
 #include <atomic>
 
@@ -35,10 +38,11 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 // LDS: two stages of U K blocks per wavefront, each T x 16 rows of 128 bytes
-// and 64 token scales; at the end the partial sums.
+// and their scales (64 tokens per DMA); at the end the partial sums.
 template <int R, int T, int KS, int U>
 struct DecodeLds {
-  static constexpr int BLOCK = T * 2048 + 256;
+  static constexpr int SDMA = (T + 3) / 4;  // DMAs of 64 token scales
+  static constexpr int BLOCK = T * 2048 + SDMA * 256;
   static constexpr int WAVE = 2 * U * BLOCK;
   static constexpr int SUMS = KS * R * T * 1024;
   static constexpr int SIZE = KS * WAVE > SUMS ? KS * WAVE : SUMS;
@@ -88,7 +92,7 @@ __global__ __launch_bounds__(KS * 64) void k_fp8_decode(
   // columns at or past K of a last block that K ends inside are read from an
   // offset out of every range: zeros.  So a load has no branch and always the
   // same OPS vector loads, which the wait in `step` counts.
-  constexpr int OPS = U * (2 * T + 1 + 2 * R);
+  constexpr int OPS = U * (2 * T + L::SDMA + 2 * R);
   constexpr int kNonTemporal = 2;
   auto load = [&](int kb, int stage, Weights& o) {
 #pragma unroll
@@ -106,7 +110,8 @@ __global__ __launch_bounds__(KS * 64) void k_fp8_decode(
 #pragma unroll
       for (int t = 0; t < 2 * T; ++t)
         dma16(rx, dst + t * 1024, (int)(out ? kOutOfRange : xsrc[t]), k * 128);
-      dma4(rs, dst + T * 2048, lane * 4, 0);
+#pragma unroll
+      for (int t = 0; t < L::SDMA; ++t) dma4(rs, dst + T * 2048 + t * 256, lane * 4 + t * 256, 0);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         o.s[u][r] = wsrow[r][k];  // block 0's past KB; `compute` takes zero there
@@ -215,19 +220,66 @@ static hipError_t run_decode(const Fp8Call& c, hipStream_t st) {
   return hipGetLastError();
 }
 
-#ifndef DR
-#define DR 1
-#define DKS 8
-#define DU 1
-#endif
+// Token blocks of the kernel that M tokens take: as many as they need up to
+// 4, then 6 or 8.
+static int token_blocks(int M) {
+  const int T = (M + 15) / 16;
+  return T <= 4 ? T : (T + 1) / 2 * 2;
+}
+
+// Feature blocks per workgroup.  A CU takes in a bounded rate of operands, so
+// the time goes with the most loaded CU's rounds of workgroups times the
+// blocks it reads per K block in each, R of the weight and T of the tokens;
+// the choice that makes that least (ties: fewer) is the fastest or within 4 %
+// of it at 28 measured shapes of 9 to 128 tokens (32x5120x5120, R = 1, 2, 3, 4,
+// 5: 12.0, 9.3, 11.2, 12.9, 13.6 us; 64x12288x36864, R = 1, 3, 5, 9: 155.6,
+// 95.8, 86.9, 75.9; 128x5120x5120, R = 1, 2, 3: 26.6, 17.8, 21.1).  At most 8
+// tokens bring little token traffic (the rows past M repeat the last one):
+// with four or more blocks per CU one block per workgroup is best, the most
+// loads in flight (1x12288x36864, R = 1, 3, 9: 65.4, 68.3, 69.9).  Above 64
+// tokens the partial sums of more than 5 blocks would not fit LDS.
+constexpr int kDecodeR[] = {1, 2, 3, 4, 5, 6, 9};
+
+Fp8DecodePlan fp8_decode_plan(int M, int N) {
+  const int cus = device_cu_count(), nrb = N / 16, T = token_blocks(M);
+  Fp8DecodePlan best{1, T, INT64_MAX};
+  for (int R : kDecodeR) {
+    if (T > 4 && R > 5) break;
+    const int64_t groups = (nrb + R - 1) / R, cost = (groups + cus - 1) / cus * (R + T);
+    if (cost < best.cost) best = Fp8DecodePlan{R, T, cost};
+    if (M <= 8 && nrb >= 4 * cus) break;
+  }
+  return best;
+}
+
+// Wavefronts that split K: eight for up to three feature and four token
+// blocks, else four (registers for twice the accumulators and weights, LDS
+// for twice the tokens).
+template <int TY, int T>
+static hipError_t decode_blocks(int R, const Fp8Call& c, hipStream_t st) {
+  constexpr int KS = T <= 4 ? 8 : 4;
+  switch (R) {
+    case 1: return run_decode<TY, 1, T, KS, 1>(c, st);
+    case 2: return run_decode<TY, 2, T, KS, 1>(c, st);
+    case 3: return run_decode<TY, 3, T, KS, 1>(c, st);
+    case 4: return run_decode<TY, 4, T, 4, 1>(c, st);
+    case 5: return run_decode<TY, 5, T, 4, 1>(c, st);
+  }
+  if constexpr (T <= 4)
+    return R == 6 ? run_decode<TY, 6, T, 4, 1>(c, st) : run_decode<TY, 9, T, 4, 1>(c, st);
+  return hipErrorInvalidValue;
+}
 
 template <int TY>
 static hipError_t decode_tokens(const Fp8Call& c, hipStream_t st) {
-  switch ((c.M + 15) / 16) {
-    case 1: return run_decode<TY, DR, 1, DKS, DU>(c, st);
-    case 2: return run_decode<TY, DR, 2, DKS, DU>(c, st);
-    case 3: return run_decode<TY, DR, 3, DKS, DU>(c, st);
-    default: return run_decode<TY, DR, 4, DKS, DU>(c, st);
+  const Fp8DecodePlan p = fp8_decode_plan(c.M, c.N);
+  switch (p.T) {
+    case 1: return decode_blocks<TY, 1>(p.R, c, st);
+    case 2: return decode_blocks<TY, 2>(p.R, c, st);
+    case 3: return decode_blocks<TY, 3>(p.R, c, st);
+    case 4: return decode_blocks<TY, 4>(p.R, c, st);
+    case 6: return decode_blocks<TY, 6>(p.R, c, st);
+    default: return decode_blocks<TY, 8>(p.R, c, st);
   }
 }
 

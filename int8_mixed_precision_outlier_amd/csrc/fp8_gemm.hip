@@ -31,17 +31,17 @@ namespace {
 
 constexpr int kMaxKB = 65536 / kFp8Block;
 
-// LDS of a tile: two stages of one K block each (W's half blocks, then X's
+// LDS of a tile: S stages of one K block each (W's half blocks, then X's
 // rows), the token scales [stage][wavefront][its tokens], the tile's weight
-// scales [128-feature block][KB + 2], and its bias in fp32.
-template <int BM, int BN, int WM, int WN>
+// scales [128-feature block][KB + S], and its bias in fp32.
+template <int BM, int BN, int WM, int WN, int S>
 struct GemmLds {
   static constexpr int STAGE = (BM + BN) * 128;
-  static constexpr int SX = 2 * STAGE;
-  static constexpr int SB = SX + 2 * WN * BM * 4;
+  static constexpr int SX = S * STAGE;
+  static constexpr int SB = SX + S * WN * BM * 4;
   static constexpr int SW = SB + BN * 4;
   static constexpr int NBT = BN > 128 ? BN / 128 : 1;
-  static constexpr int MAX = SW + NBT * (kMaxKB + 2) * 4;
+  static constexpr int MAX = SW + NBT * (kMaxKB + S) * 4;
   static_assert(MAX <= 160 * 1024, "LDS budget");
 };
 
@@ -89,12 +89,12 @@ __device__ __forceinline__ void store32(const v4f& ya, const v4f& yb, int nb, in
 
 }  // namespace
 
-template <int T, int BM, int BN, int WM, int WN>
+template <int T, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     const uint8_t* __restrict__ X, const float* __restrict__ xs, const uint8_t* __restrict__ W,
     const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y,
     int M, int N, int K, int KB, int tilesM, int tilesN, int groupM, int nbase) {
-  using L = GemmLds<BM, BN, WM, WN>;
+  using L = GemmLds<BM, BN, WM, WN, S>;
   constexpr int NWAVE = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int FM = WTM / 16, FN = WTN / 16;
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   // its token scales
   constexpr int XDMA = BM / 8 / NWAVE, HDMA = BN / 16 / NWAVE, SDMA = WTM / 64;
   static_assert(BN / 16 % NWAVE == 0 && BM / 8 % NWAVE == 0 && WTM % 64 == 0, "DMA split");
-  static_assert(128 % WTN == 0 && FN % 4 == 0 && FM >= 4, "a wavefront's features share a scale block");
+  static_assert(128 % WTN == 0 && FN % 2 == 0 && FM >= 4, "a wavefront's features share a scale block");
   extern __shared__ __align__(16) int8_t smem[];
 
   const int Tt = tilesM * tilesN;
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   float* sw = reinterpret_cast<float*>(smem + L::SW);
   float* sb = reinterpret_cast<float*>(smem + L::SB);
   const int nbs = (N + kFp8Block - 1) / kFp8Block;
-  const int KS = KB + 2;  // two zeros behind each block's scales
+  const int KS = KB + S;  // zeros behind each block's scales
   auto weight_scale = [&](int i) {
     const int nb = min(n0 / kFp8Block + i / KS, nbs - 1), kb = i % KS;
     return kb < KB ? ws[(size_t)nb * KB + kb] : 0.0f;
@@ -171,7 +171,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   // wavefront counts the same number of DMAs.  In a last block that K ends
   // inside, chunks at or past K read from an offset out of every range
   // (zeros); tokens past M read zero scales.
-  constexpr int OPA = XDMA + SDMA + HDMA, OPB = HDMA;
+  constexpr int OPA = XDMA + SDMA + HDMA, OPB = HDMA, OPS = OPA + OPB;
+  constexpr int AHEAD = (S - 1) * OPS;  // DMAs that may be in flight at a barrier
   auto dma_w = [&](int kb, int stage, int h, int j) {
     const bool live = kb < KB;
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
@@ -205,136 +206,201 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     }
   };
 
+  auto dma_one = [&](int kb, int stage, int d) {
+    if (d < OPA) dma_a(kb, stage, d, d + 1);
+    else dma_b(kb, stage, d - OPA, d - OPA + 1);
+  };
+
+  constexpr bool DB = S > 2;  // two K blocks' fragments in registers
+  static_assert(DB ? FN <= 4 : FN % 4 == 0, "registers; whole halves of W");
   v4f acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = v4f{};
 
-  // Operand fragments: two weight fragments (the next feature block's loaded
-  // under the current one's MFMAs), the tokens' FM fragments and scales of
-  // the current K block; and the last four partial products, each scaled in
-  // kLag MFMAs after its own.
+  // The last four partial products, each scaled in kLag MFMAs after its own.
   constexpr int kLag = 3;
-  v8i fw[2], fx[FM];
-  float sx[FM], s[FM] = {};
-  float s_w = 0.0f;
   v4f p[4] = {};
-  // LDS offsets of the lane's fragments and scales in either stage.  The
-  // empty asm hides that one is the other plus a constant: as immediate
-  // offsets of the reads the constants do not fit, and would be added anew
-  // in front of each.
-  int wo[2], xlo[2], xhi[2];
+  float s[FM] = {};
+  auto scale_in = [&](int o) {
 #pragma unroll
-  for (int st = 0; st < 2; ++st) {
-    wo[st] = st * L::STAGE + (wn * WTN / 16) * 2048 + lane * 16;
-    const int xo = st * L::STAGE + BN * 128 + (wm * WTM + r16) * 128;
-    xlo[st] = xo + (q4 ^ (r16 & 7)) * 16;
-    xhi[st] = xo + ((q4 + 4) ^ (r16 & 7)) * 16;
-    asm volatile("" : "+v"(wo[st]), "+v"(xlo[st]), "+v"(xhi[st]));
-  }
-  const float* sbase = reinterpret_cast<const float*>(smem + L::SX) + w * WTM + r16;
+    for (int e = 0; e < 4; ++e)
+      acc[o / FM][o % FM][e] = fmaf(p[o & 3][e], s[o % FM], acc[o / FM][o % FM][e]);
+  };
+  // MFMA number n of a K block, and the scaling of the one kLag before it;
+  // sx, s_w: the K block's scales, which count from its product 0 on
+  auto mma = [&](int n, const v8i& fw, const v8i& fx, const float(&sx)[FM], float s_w) {
+    p[n & 3] = mfma16_e4m3(fw, fx);
+    if (n == kLag) {  // the previous block's products are all in
+#pragma unroll
+      for (int q = 0; q < FM; ++q) s[q] = sx[q] * s_w;
+    }
+    scale_in((n + FN * FM - kLag) % (FN * FM));
+  };
+  // LDS offsets of the lane's fragments within a stage, and its reads
+  const int wo = (wn * WTN / 16) * 2048 + lane * 16;
+  const int xo = BN * 128 + (wm * WTM + r16) * 128;
+  const int xlo = xo + (q4 ^ (r16 & 7)) * 16, xhi = xo + ((q4 + 4) ^ (r16 & 7)) * 16;
   auto join = [](const v4i& lo, const v4i& hi) {
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  auto read_w = [&](int stage, int i, v8i& f) {
-    const int8_t* q = smem + wo[stage] + i * 2048;
-    f = join(*reinterpret_cast<const v4i*>(q), *reinterpret_cast<const v4i*>(q + 1024));
+  auto read_w = [&](int at, int i) {
+    const int8_t* q = smem + at + i * 2048;
+    return join(*reinterpret_cast<const v4i*>(q), *reinterpret_cast<const v4i*>(q + 1024));
   };
-  auto read_x = [&](int stage, int j, v8i& f) {
-    f = join(*reinterpret_cast<const v4i*>(smem + xlo[stage] + j * 2048),
-             *reinterpret_cast<const v4i*>(smem + xhi[stage] + j * 2048));
+  auto read_x = [&](int lo, int hi, int j) {
+    return join(*reinterpret_cast<const v4i*>(smem + lo + j * 2048),
+                *reinterpret_cast<const v4i*>(smem + hi + j * 2048));
   };
-  auto read_s = [&](int stage, int kb) {
+  const float* sbase = reinterpret_cast<const float*>(smem + L::SX) + w * WTM + r16;
+  auto read_s = [&](int stage, int kb, float(&sx)[FM], float& s_w) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) sx[j] = sbase[stage * NWAVE * WTM + j * 16];
     s_w = my_sw[kb];
   };
-  auto scale_in = [&](int i, int j, const v4f& v) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(v[e], s[j], acc[i][j][e]);
-  };
 
   if (KB > 0) {
-    dma_a(0, 0, 0, OPA);
-    dma_b(0, 0, 0, OPB);
-    dma_a(1, 1, 0, OPA);
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      dma_a(k, k, 0, OPA);
+      if (DB || k < S - 1) dma_b(k, k, 0, OPB);
+    }
   }
   if (t < BN) sb[t] = to_f32<T>(bias_first);
-  if (KB > 0) {
+  if (KB > 0)
     for (int i = t; i < L::NBT * KS; i += NWAVE * 64) sw[i] = i == t ? sw_first : weight_scale(i);
-    barrier_vm<OPA + OPB>();  // the weight scales, and the first DMAs of block 0
-    read_s(0, 0);
+
+  if constexpr (DB) {
+    // 64 x 64 per wavefront: the registers hold all fragments of two K blocks.
+    // The next block's are read under the current one's MFMAs, which so never
+    // wait for LDS, and a K block needs one barrier: its stage is free as
+    // soon as the fragments are in registers.  Its DMAs run S - 1 blocks ahead.
+    v8i fw[2][FN], fx[2][FM];
+    float sx[2][FM], s_w[2];
+    auto read = [&](int stage, int f, v8i(&gw)[FN], v8i(&gx)[FM]) {  // in the order of use
+      const int base = stage * L::STAGE;
+      if (f == 0) gw[0] = read_w(base + wo, 0);
+      else if (f <= FM) gx[f - 1] = read_x(base + xlo, base + xhi, f - 1);
+      else gw[f - FM] = read_w(base + wo, f - FM);
+    };
+    if (KB > 0) {
+      barrier_vm<(S - 1) * OPS>();  // the weight scales, and K block 0
 #pragma unroll
-    for (int j = 0; j < FM; ++j) read_x(0, j, fx[j]);
-    read_w(0, 0, fw[0]);
-  }
-  auto step = [&](auto ST, int kb) {
-    constexpr int st = decltype(ST)::value;
-    // feature block i of K block kb; `with(j)` issues loads after MFMA j
-    auto group = [&](auto I, auto&& with) {
-      constexpr int i = decltype(I)::value;
+      for (int f = 0; f < FM + FN; ++f) read(0, f, fw[0], fx[0]);
+      read_s(0, 0, sx[0], s_w[0]);
+      barrier_vm<(S - 2) * OPS>();  // stage 0 is free, K block 1 has landed
+    }
+    int st = 0;
+    auto step = [&](auto P, int kb) {
+      constexpr int c = decltype(P)::value;  // the parity of kb
+      const int sn = st + 1 == S ? 0 : st + 1;
+      auto block = [&](auto I) {
+        constexpr int i = decltype(I)::value;
+        constexpr int d0 = i * OPS / FN, d1 = (i + 1) * OPS / FN;
+        constexpr int R = (FM + FN) / FN;  // fragments read under a feature block
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+          mma(i * FM + j, fw[c][i], fx[c][j], sx[c], s_w[c]);
+          if (j < R) read(sn, i * R + j, fw[c ^ 1], fx[c ^ 1]);
+        }
+        if constexpr (i == FN - 1) read_s(sn, kb + 1, sx[c ^ 1], s_w[c ^ 1]);
+#pragma unroll
+        for (int d = d0; d < d1; ++d) dma_one(kb + S, st, d);
+        order<FM, 2, (R > 2 ? 2 : 1), d1 - d0>();
+      };
+      unroll(block, std::make_integer_sequence<int, FN>{});
+      // every wavefront holds K block kb + 1, whose stage may be overwritten,
+      // and its DMAs of kb + 2 have landed (since then issued: those of the
+      // S - 2 blocks kb + 3 .. kb + S)
+      barrier_vm<(S - 2) * OPS>();
+      __builtin_amdgcn_sched_barrier(0);
+      st = sn;
+    };
+    for (int kb = 0; kb < KB; kb += 2) {  // behind an odd KB a block of zeros
+      step(std::integral_constant<int, 0>{}, kb);
+      step(std::integral_constant<int, 1>{}, kb + 1);
+    }
+  } else {
+    // 64 x 128 per wavefront: the registers hold two weight fragments (the next
+    // feature block's loaded under the current one's MFMAs) and the tokens'
+    // FM fragments.  X and the two halves of W leave their stages separately,
+    // at two barriers per K block, so that their DMAs run S - 0.5 blocks ahead
+    // in S stages (one barrier and S - 1.15 blocks: 4096x12288x49152 2066 us
+    // against 1967).
+    v8i fw[2], fx[FM];
+    float sx[FM], s_w = 0.0f;
+    // the stages' offsets; the empty asm hides that one is another plus a
+    // constant: as immediate offsets of the reads the constants do not fit,
+    // and would be added anew in front of each
+    int wst[S], lst[S], hst[S];
+#pragma unroll
+    for (int st = 0; st < S; ++st) {
+      wst[st] = st * L::STAGE + wo;
+      lst[st] = st * L::STAGE + xlo;
+      hst[st] = st * L::STAGE + xhi;
+      asm volatile("" : "+v"(wst[st]), "+v"(lst[st]), "+v"(hst[st]));
+    }
+    if (KB > 0) {
+      barrier_vm<AHEAD>();  // the weight scales, and the first DMAs of block 0
+      read_s(0, 0, sx, s_w);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) fx[j] = read_x(lst[0], hst[0], j);
+      fw[0] = read_w(wst[0], 0);
+    }
+    auto step = [&](auto ST, int kb) {
+      constexpr int st = decltype(ST)::value, sn = (st + 1) % S;
+      auto upto = [&](auto I) {
+        constexpr int i = decltype(I)::value;
+        constexpr int A = FN / 2 - 1;  // first feature block after the first barrier
+        // the DMAs a barrier has made room for, spread over the feature blocks
+        // up to the other barrier: a burst fills the address unit's queue and
+        // holds up the MFMAs behind it
+        constexpr int a0 = i < A ? 0 : (i - A) * OPA / (FN - 1 - A);
+        constexpr int a1 = i < A ? 0 : (i + 1 - A) * OPA / (FN - 1 - A);
+        constexpr int b0 = i < A ? i * OPB / A : 0, b1 = i < A ? (i + 1) * OPB / A : 0;
+        static_assert(A > 0, "");
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+          mma(i * FM + j, fw[i & 1], fx[j], sx, s_w);
+          if (j == 0) fw[(i + 1) & 1] = read_w(wst[st], i + 1);
+        }
+        dma_a(kb + S, st, a0, a1);
+        dma_b(kb + S - 1, (st + S - 1) % S, b0, b1);
+        order<FM, 2, 0, a1 - a0 + b1 - b0>();
+        if constexpr (i == A - 1) {
+          // every wavefront has read X and the first half of W of this K block,
+          // and its DMAs of the second half have landed (issued S - 0.5 K blocks
+          // ago; since then the A and B parts of kb + 1 .. kb + S - 1)
+          barrier_vm<AHEAD>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      unroll(upto, std::make_integer_sequence<int, FN - 1>{});
+      // every wavefront has read the second half of W, and its DMAs of the next
+      // K block's X and first half of W have landed (since then issued: the B
+      // parts of kb + 1 .. kb + S - 1 and the A parts of kb + 2 .. kb + S)
+      barrier_vm<AHEAD>();
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
-        const int n = i * FM + j, o = (n + FN * FM - kLag) % (FN * FM);
-        p[n & 3] = mfma16_e4m3(fw[i & 1], fx[j]);
-        if (n == kLag) {  // the previous block's products are all in
-#pragma unroll
-          for (int q = 0; q < FM; ++q) s[q] = sx[q] * s_w;
-        }
-        scale_in(o / FM, o % FM, p[o & 3]);
-        with(j);
+        mma((FN - 1) * FM + j, fw[(FN - 1) & 1], fx[j], sx, s_w);
+        if (j == 0) fw[0] = read_w(wst[sn], 0);
+        fx[j] = read_x(lst[sn], hst[sn], j);
       }
+      read_s(sn, kb + 1, sx, s_w);
+      order<FM, 4, 3, 0>();
     };
-    auto upto = [&](auto I) {
-      constexpr int i = decltype(I)::value;
-      constexpr int A = FN / 2 - 1;  // first feature block after the first barrier
-      // the DMAs a barrier has made room for, spread over the feature blocks
-      // up to the other barrier: a burst fills the address unit's queue and
-      // holds up the MFMAs behind it
-      constexpr int a0 = i < A ? 0 : (i - A) * OPA / (FN - 1 - A);
-      constexpr int a1 = i < A ? 0 : (i + 1 - A) * OPA / (FN - 1 - A);
-      constexpr int b0 = i < A ? i * OPB / A : 0, b1 = i < A ? (i + 1) * OPB / A : 0;
-      static_assert(A > 0, "");
-      group(I, [&](int j) {
-        if (j == 0) read_w(st, i + 1, fw[(i + 1) & 1]);
-      });
-      dma_a(kb + 2, st, a0, a1);
-      dma_b(kb + 1, st ^ 1, b0, b1);
-      order<FM, 2, 0, a1 - a0 + b1 - b0>();
-      if constexpr (i == A - 1) {
-        // every wavefront has read X and the first half of W of this K block,
-        // and its DMAs of the second half have landed (issued 1.5 K blocks
-        // ago; since then the A part of kb + 1 and the B part of kb + 1)
-        barrier_vm<OPA + OPB>();
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    unroll(upto, std::make_integer_sequence<int, FN - 1>{});
-    // every wavefront has read the second half of W, and its DMAs of the next
-    // K block's X and first half of W have landed (since then issued: the B
-    // part of kb + 1 and the A part of kb + 2)
-    barrier_vm<OPA + OPB>();
-    __builtin_amdgcn_sched_barrier(0);
-    group(std::integral_constant<int, FN - 1>{}, [&](int j) {
-      if (j == 0) read_w(st ^ 1, 0, fw[0]);
-      read_x(st ^ 1, j, fx[j]);
-    });
-    read_s(st ^ 1, kb + 1);
-    order<FM, 4, 3, 0>();
-  };
-  // two K blocks per iteration, so that the stage is a constant in each; an
-  // odd KB ends with a block of zero operands and zero scales
-  for (int kb = 0; kb < KB; kb += 2) {
-    step(std::integral_constant<int, 0>{}, kb);
-    step(std::integral_constant<int, 1>{}, kb + 1);
+    // S K blocks per iteration, so that the stage is a constant in each; behind
+    // the last come blocks of zero operands and zero scales
+    for (int kb = 0; kb < KB; kb += S)
+      unroll([&](auto ST) { step(ST, kb + decltype(ST)::value); },
+             std::make_integer_sequence<int, S>{});
   }
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no DMA may still write LDS
   if (KB == 0) __syncthreads();              // the bias
-  if (KB > 0) {
 #pragma unroll
-    for (int o = FN * FM - kLag; o < FN * FM; ++o) scale_in(o / FM, o % FM, p[o & 3]);
-  }
+  for (int o = FN * FM - kLag; o < FN * FM; ++o) scale_in(o);
 
   // two feature blocks at a time: each token's 64 bytes leave in one store
 #pragma unroll
@@ -350,13 +416,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
 
 // One launch over the features [nbase, nend); nend is N, or a multiple of BN
 // above nbase.
-template <int T, int BM, int BN, int WM, int WN>
+template <int T, int BM, int BN, int WM, int WN, int S>
 static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st) {
-  using L = GemmLds<BM, BN, WM, WN>;
+  using L = GemmLds<BM, BN, WM, WN, S>;
   const int KB = (c.K + kFp8Block - 1) / kFp8Block;
-  const int shm = L::SW + L::NBT * (KB + 2) * 4;
+  const int shm = L::SW + L::NBT * (KB + S) * 4;
   const int tilesM = (c.M + BM - 1) / BM, tilesN = (nend - nbase + BN - 1) / BN;
-  auto kern = k_fp8_gemm<T, BM, BN, WM, WN>;
+  auto kern = k_fp8_gemm<T, BM, BN, WM, WN, S>;
   // the dynamic-LDS limit is raised once per device the kernels run on
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
@@ -379,60 +445,68 @@ static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st
 template <int T>
 static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipStream_t st) {
   switch (cfg) {
-    case kTile128: return run_gemm<T, 128, 128, 2, 2>(c, nbase, nend, st);
-    case kTile256x128: return run_gemm<T, 256, 128, 4, 2>(c, nbase, nend, st);
-    default: return run_gemm<T, 256, 256, 4, 2>(c, nbase, nend, st);
+    case kTile128Deep: return run_gemm<T, 128, 128, 2, 4, 4>(c, nbase, nend, st);
+    case kTile128: return run_gemm<T, 128, 128, 2, 2, 2>(c, nbase, nend, st);
+    case kTile256x128: return run_gemm<T, 256, 128, 4, 2, 3>(c, nbase, nend, st);
+    default: return run_gemm<T, 256, 256, 4, 2, 2>(c, nbase, nend, st);
   }
 }
 
-// Tile configuration.  The cost of a launch is counted in rounds of
-// workgroups over the chip, in units of a round of 256x256 tiles (8
-// wavefronts of 64 tokens x 128 features, one workgroup per CU), fitted at
-// K = 4096 and 5120 (us; 256x256 / 256x128 / 128x128 tiles):
-//   256x128  0.70 per round (one workgroup per CU; 2048x4096x4096: 49.4 /
-//            36.6 / 37.5);
-//   128x128  0.76 per round of two workgroups per CU, 0.42 for a last round
-//            of at most one per CU (512x5120x5120: 52.9 / 35.3 / 26.3,
-//            512x5120x20480: 62.5 / 83.4 / 75.0).
+// Kernel and tile configuration.  The cost of a launch is counted in rounds
+// of workgroups over the chip, in units of a round of 256x256 tiles (8
+// wavefronts of 64 tokens x 128 features, one workgroup per CU: 57-66 us at K
+// = 5120), fitted at K = 4096 and 5120 (us; 256x256 / 256x128 / 128x128):
+//   256x128  0.70 per round (one workgroup per CU; 2048x4096x4096: 46.4 /
+//            35.9 / 37.2);
+//   128x128  0.74 per round of two workgroups per CU (512x5120x20480: 62.0 /
+//            80.1 / 74.4); a last round of at most one per CU takes 0.42,
+//            in the form with four stages and eight wavefronts
+//            (256x5120x5120: 52.9 / 33.4 / 23.0, with two stages and four
+//            wavefronts 25.8);
+//   decode   0.030 per block of 16 features or tokens that the most loaded CU
+//            reads per K block (77x5136x20464: 29.0 us against 30.1 of 128x128
+//            tiles, 128x5120x5120: 17.8 against 22.4, 128x12288x49152: 161
+//            against 144).
 // When 256x256 tiles would leave the last round partly empty, the features
 // can be split: [0, n1) in whole rounds of 256x256 tiles, [n1, N) in a second
 // launch of smaller tiles (kGap for its fill and drain, taken when it saves
 // more than kMargin).
-constexpr double kF128 = 0.76, kF128Half = 0.42, kF256x128 = 0.70, kGap = 0.04, kMargin = 0.05;
+constexpr double kF128 = 0.74, kF128Deep = 0.42, kF256x128 = 0.70, kFDecode = 0.030, kGap = 0.04,
+                 kMargin = 0.05;
 
-static double tile_cost(int cfg, long M, long N, long cus) {
-  if (cfg == kTile128) {
-    const long t = (M + 127) / 128 * ((N + 127) / 128), rest = t % (2 * cus);
-    return kF128 * (double)(t / (2 * cus)) + (rest == 0 ? 0.0 : rest <= cus ? kF128Half : kF128);
+// The cheapest single launch over n features; ties keep the larger tile.
+static int cheapest_tile(long M, long n, long cus, double* cost) {
+  const long tm = (M + 255) / 256, t128 = (M + 127) / 128 * ((n + 127) / 128);
+  int best = kTile256;
+  *cost = (double)((tm * ((n + 255) / 256) + cus - 1) / cus);
+  const double c1 = kF256x128 * (double)((tm * ((n + 127) / 128) + cus - 1) / cus);
+  if (c1 < *cost) {
+    best = kTile256x128;
+    *cost = c1;
   }
-  const long bn = cfg == kTile256 ? 256 : 128;
-  const long t = (M + 255) / 256 * ((N + bn - 1) / bn);
-  return (cfg == kTile256 ? 1.0 : kF256x128) * (double)((t + cus - 1) / cus);
+  const double c2 = t128 <= cus ? kF128Deep
+                                : kF128 * (double)(t128 / (2 * cus)) +
+                                      (t128 % (2 * cus) == 0 ? 0.0 : t128 % (2 * cus) <= cus ? kF128Deep : kF128);
+  if (c2 < *cost) {
+    best = t128 <= cus ? kTile128Deep : kTile128;
+    *cost = c2;
+  }
+  return best;
 }
 
 Fp8Plan fp8_plan(int M, int N) {
   const long cus = device_cu_count();
-  auto cheapest = [&](long n, double* cost) {  // ties keep the larger tile
-    int best = kTile256;
-    *cost = tile_cost(kTile256, M, n, cus);
-    for (int c : {kTile256x128, kTile128}) {
-      const double v = tile_cost(c, M, n, cus);
-      if (v < *cost) {
-        best = c;
-        *cost = v;
-      }
-    }
-    return best;
-  };
   double cbest;
-  Fp8Plan best{cheapest(N, &cbest), N, 0};
+  Fp8Plan best{cheapest_tile(M, N, cus, &cbest), N, 0};
+  if (M <= kFp8DecodeMaxM && (M <= 64 || kFDecode * (double)fp8_decode_plan(M, N).cost < cbest))
+    return Fp8Plan{kDecode, N, 0};
   const long tm = (M + 255) / 256, t256 = tm * ((N + 255) / 256);
   for (long R = 1; R * cus < t256; ++R) {
     const long n1 = R * cus / tm * 256;
     if (n1 <= 0 || n1 >= N) continue;
     double rest;
-    const int second = cheapest(N - n1, &rest);
-    const double c = tile_cost(kTile256, M, n1, cus) + kGap + rest;
+    const int second = cheapest_tile(M, N - n1, cus, &rest);
+    const double c = (double)((tm * (n1 / 256) + cus - 1) / cus) + kGap + rest;
     if (second != kTile256 && c < cbest - kMargin) {
       best = Fp8Plan{kTile256, (int)n1, second};
       cbest = c;
@@ -444,13 +518,13 @@ Fp8Plan fp8_plan(int M, int N) {
 template <int T>
 static hipError_t run_matmul(const Fp8Call& c, hipStream_t st) {
   const Fp8Plan p = fp8_plan(c.M, c.N);
+  if (p.first == kDecode) return launch_fp8_decode(c, st);
   const hipError_t e = run_tiles<T>(p.first, c, 0, p.n1, st);
   if (e != hipSuccess || p.n1 >= c.N) return e;
   return run_tiles<T>(p.second, c, p.n1, c.N, st);
 }
 
 hipError_t launch_fp8_matmul(const Fp8Call& c, hipStream_t st) {
-  if (c.M <= kFp8DecodeMaxM) return launch_fp8_decode(c, st);
   return c.type == kF16 ? run_matmul<kF16>(c, st) : run_matmul<kBf16>(c, st);
 }
 
