@@ -455,6 +455,18 @@ int fp8_matmul(const void *X_f8, const float *x_scale, int64_t M, int64_t K,
                const void *bias, int type, void *Y, hipStream_t stream);
 
 /*
+ * The kernels fp8_matmul launches for an M x K x N call on the current device;
+ * host only, as int8mm_kernel_config.  cfg[4]:
+ *   weight-streaming kernel (M <= 64, and up to 128 where it is faster than
+ *     the tiles): {0, blocks of 16 features per workgroup (1-6, 9), blocks of
+ *     16 tokens (1-4, 6, 8), 0};
+ *   tiles: {1, tile rows, tile columns, LDS stages};
+ *   tiles in two launches: {2, n1, tile columns, LDS stages of the second}:
+ *     features [0, n1) in 256x256 tiles, [n1, N) in smaller ones.
+ */
+int fp8_matmul_config(int64_t M, int64_t N, int64_t K, int32_t *cfg);
+
+/*
  * Profiling aid (not thread-safe; for benchmarks).  While enabled, every
  * int8_mixed_matmul call has the dispatch of its main kernel (the tiled
  * int8 GEMM, or the decode kernel for M <= 32) record a pair of HIP events

@@ -26,7 +26,7 @@ __all__ = [
     "kernel_config", "outlier_cache_size", "build_outlier_cache", "mixed_matmul_cached",
     "STATUS_OK", "STATUS_EINVAL", "STATUS_EALIGN", "STATUS_EWORKSPACE", "STATUS_EHIP",
     "FP8_BLOCK", "fp8_kpad", "fp8_pack_weight", "fp8_quantize_weight", "fp8_quantize",
-    "fp8_rms_norm", "fp8_silu_mul", "fp8_matmul",
+    "fp8_rms_norm", "fp8_silu_mul", "fp8_matmul", "fp8_matmul_config",
     "STATUS_ESCRATCH", "FLAG_OVERFLOW", "FLAG_CACHE_MISS", "FLAG_CACHE_MISMATCH",
 ]
 
@@ -113,6 +113,8 @@ def load() -> ctypes.CDLL:
     lib.fp8_silu_mul.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _vp]
     lib.fp8_matmul.restype = ctypes.c_int
     lib.fp8_matmul.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _vp]
+    lib.fp8_matmul_config.restype = ctypes.c_int
+    lib.fp8_matmul_config.argtypes = [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_int32)]
     _lib = lib
     return lib
 
@@ -499,5 +501,5 @@ def timing_read():
     return ms.value, n.value
 
 
-from .fp8 import (FP8_BLOCK, fp8_kpad, fp8_matmul, fp8_pack_weight, fp8_quantize,  # noqa: E402
-                  fp8_quantize_weight, fp8_rms_norm, fp8_silu_mul)
+from .fp8 import (FP8_BLOCK, fp8_kpad, fp8_matmul, fp8_matmul_config, fp8_pack_weight,  # noqa: E402
+                  fp8_quantize, fp8_quantize_weight, fp8_rms_norm, fp8_silu_mul)

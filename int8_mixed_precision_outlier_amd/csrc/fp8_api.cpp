@@ -112,4 +112,28 @@ int fp8_matmul(const void* X_f8, const float* x_scale, int64_t M, int64_t K, con
   return hip_error_status(launch_fp8_matmul(c, stream));
 }
 
+int fp8_matmul_config(int64_t M, int64_t N, int64_t K, int32_t* cfg) {
+  int st = check_rows(INT8MM_F16, M, K, K);
+  if (st != INT8MM_OK) return st;
+  st = check_weight(K, N);
+  if (st != INT8MM_OK) return st;
+  if (!cfg || M == 0 || N == 0 || M * N > INT8MM_MAX_MN) return INT8MM_EINVAL;
+  struct Tile {
+    int32_t bm, bn, stages;
+  };
+  static constexpr Tile kTiles[] = {{256, 256, 2}, {256, 128, 3}, {128, 128, 2}, {128, 128, 4}};
+  const Fp8Plan p = fp8_plan((int)M, (int)N);
+  if (p.first == kDecode) {
+    const Fp8DecodePlan d = fp8_decode_plan((int)M, (int)N);
+    cfg[0] = 0, cfg[1] = d.R, cfg[2] = d.T, cfg[3] = 0;
+  } else if (p.n1 >= N) {
+    const Tile t = kTiles[p.first];
+    cfg[0] = 1, cfg[1] = t.bm, cfg[2] = t.bn, cfg[3] = t.stages;
+  } else {
+    const Tile t = kTiles[p.second];
+    cfg[0] = 2, cfg[1] = p.n1, cfg[2] = t.bn, cfg[3] = t.stages;
+  }
+  return INT8MM_OK;
+}
+
 }  // extern "C"

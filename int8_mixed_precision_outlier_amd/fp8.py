@@ -20,10 +20,10 @@ import ctypes
 
 import torch
 
-from . import _check, _ptr, load
+from . import _check, load
 
 __all__ = ["FP8_BLOCK", "fp8_kpad", "fp8_pack_weight", "fp8_quantize_weight", "fp8_quantize",
-           "fp8_rms_norm", "fp8_silu_mul", "fp8_matmul"]
+           "fp8_rms_norm", "fp8_silu_mul", "fp8_matmul", "fp8_matmul_config"]
 
 FP8_BLOCK = 128
 _E4M3 = torch.float8_e4m3fn
@@ -42,13 +42,15 @@ def _blocks(n: int) -> int:
 def _tensor(t, name: str, dtypes, shape, device=None):
     """A contiguous GPU tensor of one of `dtypes` and of `shape` (None: any
     size), on `device` if given."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+    have = t.shape
+    if have != shape and (len(have) != len(shape)
+                          or any(w is not None and h != w for h, w in zip(have, shape))):
         want = tuple("any" if w is None else w for w in shape)
-        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must have shape {want}, got {tuple(have)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
@@ -56,17 +58,34 @@ def _tensor(t, name: str, dtypes, shape, device=None):
     return t
 
 
-@contextlib.contextmanager
-def _launch(device, stream):
-    """Makes `device` (and `stream`, if given) current; yields the stream handle."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+class _Launch:
+    """Makes `device` (and `stream`, if given) current where they are not, and
+    gives the stream's handle."""
+    __slots__ = ("device", "stream", "contexts")
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        self.device, self.stream, self.contexts = device, stream, None
+
+    def __enter__(self):
+        if self.stream is None and torch.cuda.current_device() == self.device.index:
+            return torch.cuda.current_stream().cuda_stream
+        self.contexts = contextlib.ExitStack()
+        self.contexts.enter_context(torch.cuda.device(self.device))
+        if self.stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        self.contexts.enter_context(torch.cuda.stream(self.stream))
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.contexts is not None:
+            self.contexts.close()
+
+
+def _at(t):
+    """The address the library takes; None for an absent or empty tensor."""
+    return None if t is None else t.data_ptr() or None
 
 
 def _quantized(out, M, K, device):
@@ -85,9 +104,9 @@ def fp8_pack_weight(Wq: torch.Tensor, stream=None) -> torch.Tensor:
     opaque buffer)."""
     _tensor(Wq, "Wq", (_E4M3,), (None, None))
     N, K = Wq.shape
-    with _launch(Wq.device, stream) as st:
+    with _Launch(Wq.device, stream) as st:
         out = torch.empty((N, fp8_kpad(K)), dtype=_E4M3, device=Wq.device)
-        _check(load().fp8_pack_weight(_ptr(Wq), N, K, _ptr(out), st))
+        _check(load().fp8_pack_weight(_at(Wq), N, K, _at(out), st))
     return out
 
 
@@ -96,11 +115,11 @@ def fp8_quantize_weight(W: torch.Tensor, stream=None):
     [ceil(N/128), ceil(K/128)]), one scale per 128 x 128 block."""
     _tensor(W, "W", tuple(_TYPES), (None, None))
     K, N = W.shape
-    with _launch(W.device, stream) as st:
+    with _Launch(W.device, stream) as st:
         W_f8 = torch.empty((N, fp8_kpad(K)), dtype=_E4M3, device=W.device)
         w_scale = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
-        _check(load().fp8_quantize_weight(_ptr(W), _TYPES[W.dtype], K, N, _ptr(W_f8),
-                                          _ptr(w_scale), st))
+        _check(load().fp8_quantize_weight(_at(W), _TYPES[W.dtype], K, N, _at(W_f8),
+                                          _at(w_scale), st))
     return W_f8, w_scale
 
 
@@ -109,9 +128,9 @@ def fp8_quantize(X: torch.Tensor, out=None, stream=None):
     `out`: such a pair to write into."""
     _tensor(X, "X", tuple(_TYPES), (None, None))
     M, K = X.shape
-    with _launch(X.device, stream) as st:
+    with _Launch(X.device, stream) as st:
         X_f8, x_scale = _quantized(out, M, K, X.device)
-        _check(load().fp8_quantize(_ptr(X), _TYPES[X.dtype], M, K, _ptr(X_f8), _ptr(x_scale), st))
+        _check(load().fp8_quantize(_at(X), _TYPES[X.dtype], M, K, _at(X_f8), _at(x_scale), st))
     return X_f8, x_scale
 
 
@@ -131,13 +150,13 @@ def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             _tensor(residual_out, "residual_out", (X.dtype,), (M, K), X.device)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    with _launch(X.device, stream) as st:
+    with _Launch(X.device, stream) as st:
         X_f8, x_scale = _quantized(out, M, K, X.device)
         H = residual_out
         if residual is not None and H is None:
             H = torch.empty((M, K), dtype=X.dtype, device=X.device)
-        _check(load().fp8_rms_norm(_ptr(X), _ptr(residual), _ptr(weight), _TYPES[X.dtype], M, K,
-                                   ctypes.c_float(float(eps)), _ptr(H), _ptr(X_f8), _ptr(x_scale),
+        _check(load().fp8_rms_norm(_at(X), _at(residual), _at(weight), _TYPES[X.dtype], M, K,
+                                   float(eps), _at(H), _at(X_f8), _at(x_scale),
                                    st))
     return (X_f8, x_scale) if residual is None else (X_f8, x_scale, H)
 
@@ -150,10 +169,10 @@ def fp8_silu_mul(gate_up: torch.Tensor, out=None, stream=None):
     if K2 % 2:
         raise ValueError(f"gate_up must have an even number of columns, got {K2}")
     K = K2 // 2
-    with _launch(gate_up.device, stream) as st:
+    with _Launch(gate_up.device, stream) as st:
         A_f8, a_scale = _quantized(out, M, K, gate_up.device)
-        _check(load().fp8_silu_mul(_ptr(gate_up), _TYPES[gate_up.dtype], M, K, _ptr(A_f8),
-                                   _ptr(a_scale), st))
+        _check(load().fp8_silu_mul(_at(gate_up), _TYPES[gate_up.dtype], M, K, _at(A_f8),
+                                   _at(a_scale), st))
     return A_f8, a_scale
 
 
@@ -180,9 +199,21 @@ def fp8_matmul(X_f8: torch.Tensor, x_scale: torch.Tensor, W_f8: torch.Tensor,
         _tensor(bias, "bias", (out_dtype,), (N,), dev)
     if out is not None:
         _tensor(out, "out", (out_dtype,), (M, N), dev)
-    with _launch(dev, stream) as st:
+    with _Launch(dev, stream) as st:
         if out is None:
             out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        _check(load().fp8_matmul(_ptr(X_f8), _ptr(x_scale), M, K, _ptr(W_f8), _ptr(w_scale), N,
-                                 _ptr(bias), _TYPES[out_dtype], _ptr(out), st))
+        _check(load().fp8_matmul(_at(X_f8), _at(x_scale), M, K, _at(W_f8), _at(w_scale), N,
+                                 _at(bias), _TYPES[out_dtype], _at(out), st))
     return out
+
+
+def fp8_matmul_config(M: int, N: int, K: int):
+    """What fp8_matmul launches for these sizes on the current device:
+    ("decode", feature blocks of 16 per workgroup, token blocks of 16),
+    ("tiled", BM, BN, stages), or ("split", n1, BN, stages): features below n1
+    in 256x256 tiles, the rest in a second launch of smaller ones."""
+    cfg = (ctypes.c_int32 * 4)()
+    _check(load().fp8_matmul_config(M, N, K, cfg))
+    if cfg[0] == 0:
+        return ("decode", int(cfg[1]), int(cfg[2]))
+    return (("tiled", "split")[cfg[0] - 1], int(cfg[1]), int(cfg[2]), int(cfg[3]))

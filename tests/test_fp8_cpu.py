@@ -162,3 +162,38 @@ def test_binding_wants_gpu_tensors():
         Fp8BlockLinear(x)
     with pytest.raises(TypeError):
         Fp8RMSNorm(x[0])
+
+
+@needs_lib
+def test_kernel_choice_over_seeded_sizes():
+    """The planner on 256 CUs over 4000 seeded sizes: streaming up to 64 tokens
+    and only up to 128, with the token blocks the tokens need; only tiles the
+    library builds; a split only at a multiple of 256 strictly inside N, in
+    whole rounds of 256x256 tiles in front."""
+    import torch
+    if torch.cuda.is_available() and torch.cuda.get_device_properties(0).multi_processor_count != 256:
+        pytest.skip("the expected choices are those of 256 CUs")
+    rng = np.random.default_rng(77)
+    tiles = {(256, 256, 2), (256, 128, 3), (128, 128, 2), (128, 128, 4)}
+    seen = set()
+    for _ in range(4000):
+        M = int(rng.choice([rng.integers(1, 129), rng.integers(129, 6000)]))
+        N = int(np.exp(rng.uniform(0, np.log(4000)))) * 16
+        c = i8.fp8_matmul_config(M, N, 16)
+        seen.add(c[0] if c[0] == "split" else c)
+        if M <= 64 or c[0] == "decode":
+            T = -(-M // 16)
+            assert c[0] == "decode" and M <= 128 and c[1] in (1, 2, 3, 4, 5, 6, 9), (M, N, c)
+            assert c[2] == (T if T <= 4 else T + T % 2) and (T <= 4 or c[1] <= 5), (M, N, c)
+        elif c[0] == "tiled":
+            assert c[1:] in tiles, (M, N, c)
+        else:
+            assert c[0] == "split" and c[1] % 256 == 0 and 0 < c[1] < N, (M, N, c)
+            assert (256 if c[3] == 3 else 128, c[2], c[3]) in tiles - {(256, 256, 2)}, (M, N, c)
+            tm = -(-M // 256)
+            assert tm * (c[1] // 256) + tm > -(-tm * (c[1] // 256) // 256) * 256, (M, N, c)
+    assert {("tiled",) + t for t in tiles} | {"split"} <= seen
+    with pytest.raises(i8.Int8mmError):
+        i8.fp8_matmul_config(4, 24, 64)
+    with pytest.raises(i8.Int8mmError):
+        i8.fp8_matmul_config(0, 32, 64)

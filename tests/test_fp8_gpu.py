@@ -244,6 +244,59 @@ def test_matmul(M, K, N, dtype):
         check_product(Y, want, K, dtype, (M, K, N, bias is not None))
 
 
+# the smallest features at which the planner takes each count of feature
+# blocks per workgroup, with an odd last workgroup, on 256 CUs
+DECODE_N = {1: 4080, 2: 4112, 3: 8208, 4: 12304, 5: 16416, 6: 20528, 9: 32800}
+DECODE_CASES = [(M, R) for M in (1, 9, 16, 17, 32, 33, 48, 50, 64, 70, 96, 97, 128) for R in DECODE_N
+                if R <= (4 if M == 1 else 9 if M <= 64 else 5)]
+# (M, N) that take each tile, and the split launch, with ragged last tiles
+TILE_CASES = {(130, 40000): ("tiled", 256, 256, 2), (300, 16368): ("tiled", 256, 128, 3),
+              (100, 40016): ("tiled", 128, 128, 2), (200, 2064): ("tiled", 128, 128, 4),
+              (1100, 20000): ("split", 13056, 128, 2), (2048, 20464): ("split", 16384, 128, 3),
+              (1300, 11952): ("split", 10752, 128, 4)}
+
+
+@pytest.mark.parametrize("M,R", DECODE_CASES)
+def test_matmul_every_streaming_kernel(M, R):
+    """Every (feature blocks, token blocks) of the weight-streaming kernel, with
+    fewer K blocks than wavefronts and, for the small ones, more."""
+    N, T = DECODE_N[R], -(-M // 16)
+    assert i8.fp8_matmul_config(M, N, 272) == ("decode", R, T if T <= 4 else T + T % 2)
+    for K in (272, 2192) if R <= 2 else (272,):
+        xq, xs, wq, ws = operands(M, K, N, M + R)
+        b = torch.randn(N, generator=torch.Generator().manual_seed(N)).to(torch.bfloat16)
+        want = F.matmul64(xq, xs, wq, ws, f32(b))
+        Y = i8.fp8_matmul(*on_gpu(xq, xs, wq, ws), bias=b.cuda())
+        check_product(Y, want, K, torch.bfloat16, (M, K, N))
+
+
+@pytest.mark.parametrize("M,N", TILE_CASES)
+@pytest.mark.parametrize("K", [16, 144, 384, 656, 1168])
+def test_matmul_every_tile(M, N, K):
+    """Every tile shape with 1, 2, 3, 6 and 10 K blocks (fewer than, as many as
+    and more than the stages), some ending inside a block."""
+    assert i8.fp8_matmul_config(M, N, K) == TILE_CASES[M, N]
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    xq, wq = codes(M * K, 1).view(M, K), codes(N * K, 2).view(N, K)
+    xq |= torch.randint(0, 2, xq.shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+    kb, nb = -(-K // 128), -(-N // 128)
+    xs = torch.rand((kb, M), generator=g, device="cuda") * 2e-3
+    ws = torch.rand((nb, kb), generator=g, device="cuda") * 2e-4
+    Y = i8.fp8_matmul(xq.view(E4M3), xs, i8.fp8_pack_weight(wq.view(E4M3)), ws, out_dtype=torch.float16)
+    # all rows against a third of the features, the first and the last among them
+    n = np.unique(np.r_[0:N:3, 0:32, N - 32:N, 10740:10770, 13040:13070, 16370:16400])
+    n = n[n < N]
+    x, w = raw(xq), raw(wq[torch.from_numpy(n).cuda()])
+    sw = ws.cpu().numpy()[n // 128]  # a scale per feature: one "block" each
+    got = Y[:, torch.from_numpy(n).cuda()]
+    xv, wv = F.e4m3_decode(x), F.e4m3_decode(w)
+    sx, sw = F.spread_columns(xs.cpu().numpy(), K), np.repeat(sw.astype(np.float64), 128, 1)[:, :K]
+    top = lambda v: np.maximum(np.abs(v).reshape(len(v), K // 8, 8).max(2), 2.0 ** -6)  # noqa: E731
+    want = ((xv * sx) @ (wv * sw).T, np.abs(xv * sx) @ np.abs(wv * sw).T,
+            (top(xv) * sx[:, ::8]) @ (top(wv) * sw[:, ::8]).T)
+    check_product(got, want, K, torch.float16, (M, N, K))
+
+
 @pytest.mark.parametrize("M,K,N", [(1, 144, 64), (16, 2064, 272), (40, 528, 400), (150, 1024, 528), (513, 272, 784)])
 def test_matmul_exact_small_integers(M, K, N):
     """Integers -4 .. 4 with unit scales: every partial sum is exact in fp32, so
