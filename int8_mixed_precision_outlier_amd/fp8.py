@@ -28,6 +28,7 @@ __all__ = ["FP8_BLOCK", "fp8_kpad", "fp8_pack_weight", "fp8_quantize_weight", "f
 FP8_BLOCK = 128
 _E4M3 = torch.float8_e4m3fn
 _TYPES = {torch.float16: 0, torch.bfloat16: 1}  # int8mm_type
+_HALVES = tuple(_TYPES)
 
 
 def fp8_kpad(K: int) -> int:
@@ -58,29 +59,23 @@ def _tensor(t, name: str, dtypes, shape, device=None):
     return t
 
 
-class _Launch:
-    """Makes `device` (and `stream`, if given) current where they are not, and
-    gives the stream's handle."""
-    __slots__ = ("device", "stream", "contexts")
+# The current stream's handle on a device; torch.cuda.current_stream builds an
+# object around it first (3 us of a single-token call's 13)
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        self.device, self.stream, self.contexts = device, stream, None
 
-    def __enter__(self):
-        if self.stream is None and torch.cuda.current_device() == self.device.index:
-            return torch.cuda.current_stream().cuda_stream
-        self.contexts = contextlib.ExitStack()
-        self.contexts.enter_context(torch.cuda.device(self.device))
-        if self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        self.contexts.enter_context(torch.cuda.stream(self.stream))
-        return self.stream.cuda_stream
+def _elsewhere(t, stream) -> bool:
+    """Whether a call on t's device (and `stream`) has to make them current first."""
+    return stream is not None or t.get_device() != torch.cuda.current_device()
 
-    def __exit__(self, *exc):
-        if self.contexts is not None:
-            self.contexts.close()
+
+@contextlib.contextmanager
+def _current(t, stream):
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
+        yield
 
 
 def _at(t):
@@ -103,34 +98,41 @@ def fp8_pack_weight(Wq: torch.Tensor, stream=None) -> torch.Tensor:
     ceil(K/128)]) -> the packed layout, as an e4m3 tensor [N, fp8_kpad(K)] (an
     opaque buffer)."""
     _tensor(Wq, "Wq", (_E4M3,), (None, None))
+    if _elsewhere(Wq, stream):
+        with _current(Wq, stream):
+            return fp8_pack_weight(Wq)
     N, K = Wq.shape
-    with _Launch(Wq.device, stream) as st:
-        out = torch.empty((N, fp8_kpad(K)), dtype=_E4M3, device=Wq.device)
-        _check(load().fp8_pack_weight(_at(Wq), N, K, _at(out), st))
+    out = torch.empty((N, fp8_kpad(K)), dtype=_E4M3, device=Wq.device)
+    _check(load().fp8_pack_weight(_at(Wq), N, K, _at(out), _stream_of(Wq.get_device())))
     return out
 
 
 def fp8_quantize_weight(W: torch.Tensor, stream=None):
     """W fp16 or bf16 [K,N] -> (W_f8 packed e4m3 [N, fp8_kpad(K)], w_scale fp32
     [ceil(N/128), ceil(K/128)]), one scale per 128 x 128 block."""
-    _tensor(W, "W", tuple(_TYPES), (None, None))
+    _tensor(W, "W", _HALVES, (None, None))
+    if _elsewhere(W, stream):
+        with _current(W, stream):
+            return fp8_quantize_weight(W)
     K, N = W.shape
-    with _Launch(W.device, stream) as st:
-        W_f8 = torch.empty((N, fp8_kpad(K)), dtype=_E4M3, device=W.device)
-        w_scale = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
-        _check(load().fp8_quantize_weight(_at(W), _TYPES[W.dtype], K, N, _at(W_f8),
-                                          _at(w_scale), st))
+    W_f8 = torch.empty((N, fp8_kpad(K)), dtype=_E4M3, device=W.device)
+    w_scale = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
+    _check(load().fp8_quantize_weight(_at(W), _TYPES[W.dtype], K, N, _at(W_f8), _at(w_scale),
+                                      _stream_of(W.get_device())))
     return W_f8, w_scale
 
 
 def fp8_quantize(X: torch.Tensor, out=None, stream=None):
     """X fp16 or bf16 [M,K] -> (X_f8 e4m3 [M,K], x_scale fp32 [ceil(K/128), M]).
     `out`: such a pair to write into."""
-    _tensor(X, "X", tuple(_TYPES), (None, None))
+    _tensor(X, "X", _HALVES, (None, None))
+    if _elsewhere(X, stream):
+        with _current(X, stream):
+            return fp8_quantize(X, out=out)
     M, K = X.shape
-    with _Launch(X.device, stream) as st:
-        X_f8, x_scale = _quantized(out, M, K, X.device)
-        _check(load().fp8_quantize(_at(X), _TYPES[X.dtype], M, K, _at(X_f8), _at(x_scale), st))
+    X_f8, x_scale = _quantized(out, M, K, X.device)
+    _check(load().fp8_quantize(_at(X), _TYPES[X.dtype], M, K, _at(X_f8), _at(x_scale),
+                               _stream_of(X.get_device())))
     return X_f8, x_scale
 
 
@@ -141,7 +143,10 @@ def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     (X_f8, x_scale), or with `residual` [M,K], whose sum with X (rounded to
     their type) is normed instead, (X_f8, x_scale, H) with H that sum.
     `residual_out` takes H; it may be `residual` itself."""
-    _tensor(X, "X", tuple(_TYPES), (None, None))
+    _tensor(X, "X", _HALVES, (None, None))
+    if _elsewhere(X, stream):
+        with _current(X, stream):
+            return fp8_rms_norm(X, weight, eps, residual, residual_out, out)
     M, K = X.shape
     _tensor(weight, "weight", (X.dtype,), (K,), X.device)
     if residual is not None:
@@ -150,29 +155,30 @@ def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             _tensor(residual_out, "residual_out", (X.dtype,), (M, K), X.device)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    with _Launch(X.device, stream) as st:
-        X_f8, x_scale = _quantized(out, M, K, X.device)
-        H = residual_out
-        if residual is not None and H is None:
-            H = torch.empty((M, K), dtype=X.dtype, device=X.device)
-        _check(load().fp8_rms_norm(_at(X), _at(residual), _at(weight), _TYPES[X.dtype], M, K,
-                                   float(eps), _at(H), _at(X_f8), _at(x_scale),
-                                   st))
+    X_f8, x_scale = _quantized(out, M, K, X.device)
+    H = residual_out
+    if residual is not None and H is None:
+        H = torch.empty((M, K), dtype=X.dtype, device=X.device)
+    _check(load().fp8_rms_norm(_at(X), _at(residual), _at(weight), _TYPES[X.dtype], M, K,
+                               float(eps), _at(H), _at(X_f8), _at(x_scale),
+                               _stream_of(X.get_device())))
     return (X_f8, x_scale) if residual is None else (X_f8, x_scale, H)
 
 
 def fp8_silu_mul(gate_up: torch.Tensor, out=None, stream=None):
     """gate_up fp16 or bf16 [M,2K] (K gates, then K ups) -> the quantized
     silu(gate) * up: (A_f8 e4m3 [M,K], a_scale fp32 [ceil(K/128), M])."""
-    _tensor(gate_up, "gate_up", tuple(_TYPES), (None, None))
+    _tensor(gate_up, "gate_up", _HALVES, (None, None))
+    if _elsewhere(gate_up, stream):
+        with _current(gate_up, stream):
+            return fp8_silu_mul(gate_up, out=out)
     M, K2 = gate_up.shape
     if K2 % 2:
         raise ValueError(f"gate_up must have an even number of columns, got {K2}")
     K = K2 // 2
-    with _Launch(gate_up.device, stream) as st:
-        A_f8, a_scale = _quantized(out, M, K, gate_up.device)
-        _check(load().fp8_silu_mul(_at(gate_up), _TYPES[gate_up.dtype], M, K, _at(A_f8),
-                                   _at(a_scale), st))
+    A_f8, a_scale = _quantized(out, M, K, gate_up.device)
+    _check(load().fp8_silu_mul(_at(gate_up), _TYPES[gate_up.dtype], M, K, _at(A_f8), _at(a_scale),
+                               _stream_of(gate_up.get_device())))
     return A_f8, a_scale
 
 
@@ -185,6 +191,9 @@ def fp8_matmul(X_f8: torch.Tensor, x_scale: torch.Tensor, W_f8: torch.Tensor,
     [ceil(N/128), ceil(K/128)]), plus `bias` [N].  Y and bias are of
     `out_dtype` (fp16 or bf16; by default that of `out`, else of bias, else bf16)."""
     _tensor(X_f8, "X_f8", (_E4M3,), (None, None))
+    if _elsewhere(X_f8, stream):
+        with _current(X_f8, stream):
+            return fp8_matmul(X_f8, x_scale, W_f8, w_scale, bias, out_dtype, out)
     M, K = X_f8.shape
     dev = X_f8.device
     _tensor(x_scale, "x_scale", (torch.float32,), (_blocks(K), M), dev)
@@ -199,11 +208,10 @@ def fp8_matmul(X_f8: torch.Tensor, x_scale: torch.Tensor, W_f8: torch.Tensor,
         _tensor(bias, "bias", (out_dtype,), (N,), dev)
     if out is not None:
         _tensor(out, "out", (out_dtype,), (M, N), dev)
-    with _Launch(dev, stream) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        _check(load().fp8_matmul(_at(X_f8), _at(x_scale), M, K, _at(W_f8), _at(w_scale), N,
-                                 _at(bias), _TYPES[out_dtype], _at(out), st))
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _check(load().fp8_matmul(_at(X_f8), _at(x_scale), M, K, _at(W_f8), _at(w_scale), N, _at(bias),
+                             _TYPES[out_dtype], _at(out), _stream_of(X_f8.get_device())))
     return out
 
 
