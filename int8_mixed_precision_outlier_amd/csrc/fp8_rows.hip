@@ -9,6 +9,7 @@
 // The scales leave k-major, xs[kb][m]: the product reads one block's scales
 // of a tile's tokens as contiguous words.
 #include "fp8.hpp"
+#include "launch.hpp"
 
 namespace i8mm {
 
@@ -35,10 +36,20 @@ __device__ __forceinline__ uint2 quant8(const float (&y)[8], float& scale) {
                     pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
 }
 
-// silu(g) * u = g / (1 + exp(-g)) * u in fp32.  exp overflows to infinity
-// below g = -88.7, where the quotient is a signed zero, as in the limit.
+// silu(g) * u = g / (1 + exp(-g)) * u in fp32.  exp(-g) is 2^t times a
+// correction for what t = -g log2(e) loses in its rounding (and log2(e) in
+// its own), so that its error stays at the exponential instruction's, and
+// the quotient is a product with the reciprocal instruction's result: within
+// 8 half steps in all, at a third of the instructions of expf and the IEEE
+// division, which bound this kernel (2048x20480 with two blocks per group: 37.9 us; with expf and four: 50.8).  exp
+// overflows to infinity below g = -88.7, where the quotient is a signed zero,
+// as in the limit.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  return g / (1.0f + expf(-g)) * u;
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float t = -g * kLog2e;
+  const float r = fmaf(-g, kLog2eLow, fmaf(-g, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t) * fmaf(r, kLn2, 1.0f);
+  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
 }  // namespace
@@ -237,17 +248,27 @@ __global__ __launch_bounds__(256) void k_fp8_pack(const uint8_t* __restrict__ sr
 // 16 columns may have 2^27 rows.
 constexpr int kRowsPerLaunch = 1 << 20;
 
-template <int T, bool GATED>
-static hipError_t run_blocks(const void* X, int M, int K, void* Xq, float* xs, hipStream_t st) {
-  const int KB = (K + kFp8Block - 1) / kFp8Block;
-  constexpr int U = 4;
-  const int strips = (KB + U - 1) / U;
+template <int T, bool GATED, int U>
+static hipError_t run_strips(const void* X, int M, int K, void* Xq, float* xs, hipStream_t st) {
+  const int KB = (K + kFp8Block - 1) / kFp8Block, strips = (KB + U - 1) / U;
   for (int64_t m0 = 0; m0 < M; m0 += kRowsPerLaunch) {
     const int rows = (int)(M - m0 < kRowsPerLaunch ? M - m0 : kRowsPerLaunch);
     k_fp8_blocks<T, GATED, U><<<strips * ((rows + 15) / 16), 256, 0, st>>>(
         static_cast<const uint16_t*>(X), (int)m0, M, K, strips, static_cast<uint8_t*>(Xq), xs);
   }
   return hipGetLastError();
+}
+
+// One block per 16 lanes while that keeps the workgroups within one round of
+// the chip (8 per CU): the calls are then bound by latency (1x20480 gated, U =
+// 1, 2, 4: 2.5, 3.1, 4.0 us; 300x5120: 2.5, 2.8, 3.4).  Two for more: 4096x12288,
+// U = 1, 2, 4, 8: 27.4, 24.9, 25.1, 27.1 us (6.1 TB/s); 2048x20480 gated: 38.6,
+// 37.9, 38.2, 41.5 (5.6 TB/s).
+template <int T, bool GATED>
+static hipError_t run_blocks(const void* X, int M, int K, void* Xq, float* xs, hipStream_t st) {
+  const int64_t groups = ((int64_t)M + 15) / 16 * ((K + kFp8Block - 1) / kFp8Block);
+  return groups <= 8 * device_cu_count() ? run_strips<T, GATED, 1>(X, M, K, Xq, xs, st)
+                                         : run_strips<T, GATED, 2>(X, M, K, Xq, xs, st);
 }
 
 hipError_t launch_fp8_quantize(const void* X, int type, int M, int K, void* Xq, float* xs,
@@ -281,14 +302,24 @@ static hipError_t run_norm(const NormCall& c, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Threads and chunks per thread that hold a row of K <= 65536 columns.
+// Threads and chunks per thread that hold a row of K <= 65536 columns: about
+// as many threads as chunks for few rows, which wait for one row's latency
+// (1x4096, 512 x 1 against 256 x 2: 2.8 and 3.1 us; 333x4112, 512 x 2 against
+// 256 x 3: 3.6 and 3.9), fewer threads for many, which need workgroups to
+// overlap (2048x5120, 256 x 3 against 512 x 2: 12.9 and 13.6 us; 4096x12288,
+// 768 x 2, 512 x 3, 256 x 6: 67.9, 68.8, 74.8 us = 5.2 TB/s; 4000x272, 64 x 1
+// against 256 x 1: 4.1 and 4.7).
 template <int T>
 static hipError_t norm_shape(const NormCall& c, hipStream_t st) {
   const int chunks = (c.K + 7) / 8;
+  const bool few = c.M <= 2 * device_cu_count();
+  if (chunks <= 64) return run_norm<T, 64, 1>(c, st);
+  if (chunks <= 128) return run_norm<T, 128, 1>(c, st);
   if (chunks <= 256) return run_norm<T, 256, 1>(c, st);
-  if (chunks <= 512) return run_norm<T, 256, 2>(c, st);
+  if (chunks <= 512) return few ? run_norm<T, 512, 1>(c, st) : run_norm<T, 256, 2>(c, st);
+  if (chunks <= 768 && !few) return run_norm<T, 256, 3>(c, st);
   if (chunks <= 1024) return run_norm<T, 512, 2>(c, st);
-  if (chunks <= 1536) return run_norm<T, 512, 3>(c, st);
+  if (chunks <= 1536) return run_norm<T, 768, 2>(c, st);
   if (chunks <= 2048) return run_norm<T, 1024, 2>(c, st);
   if (chunks <= 4096) return run_norm<T, 1024, 4>(c, st);
   return run_norm<T, 1024, 8>(c, st);

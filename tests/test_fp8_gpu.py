@@ -140,7 +140,8 @@ def test_quantize_extremes(dtype):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("residual", [False, True])
-@pytest.mark.parametrize("M,K", ROWS + [(2, 2048), (2, 2064), (2, 4112), (1, 12304), (1, 16400), (1, 32784)])
+@pytest.mark.parametrize("M,K", ROWS + [(2, 512), (2, 1024), (2, 2048), (2, 2064), (600, 2064), (600, 4112),
+                                        (2, 8208), (1, 12304), (1, 16400), (1, 32784)])
 def test_rms_norm(M, K, residual, dtype):
     X, R = acts(M, K, dtype, K + M), acts(M, K, dtype, K + M + 1)
     g = (1 + 0.2 * acts(1, K, dtype, 5, outliers=0)[0].float()).to(dtype)
