@@ -120,7 +120,7 @@ struct Fp8Call {
 // The kernels of an M x N product.  Tiles: features [0, n1) in tiles `first`,
 // [n1, N) (if any) in tiles `second`; kDecode: the weight-streaming kernel
 // with R feature and T token blocks of 16.
-enum { kDecode = -1, kTile256 = 0, kTile256x128 = 1, kTile128 = 2, kTile128Deep = 3 };
+enum { kDecode = -1, kTile256 = 0, kTile256x128 = 1, kTile128 = 2, kTile128Deep = 3, kTile64x128 = 4 };
 struct Fp8Plan {
   int first, n1, second;
 };

@@ -121,7 +121,8 @@ int fp8_matmul_config(int64_t M, int64_t N, int64_t K, int32_t* cfg) {
   struct Tile {
     int32_t bm, bn, stages;
   };
-  static constexpr Tile kTiles[] = {{256, 256, 2}, {256, 128, 3}, {128, 128, 2}, {128, 128, 4}};
+  static constexpr Tile kTiles[] = {{256, 256, 2}, {256, 128, 3}, {128, 128, 2}, {128, 128, 4},
+                                    {64, 128, 3}};
   const Fp8Plan p = fp8_plan((int)M, (int)N);
   if (p.first == kDecode) {
     const Fp8DecodePlan d = fp8_decode_plan((int)M, (int)N);
@@ -131,7 +132,7 @@ int fp8_matmul_config(int64_t M, int64_t N, int64_t K, int32_t* cfg) {
     cfg[0] = 1, cfg[1] = t.bm, cfg[2] = t.bn, cfg[3] = t.stages;
   } else {
     const Tile t = kTiles[p.second];
-    cfg[0] = 2, cfg[1] = p.n1, cfg[2] = t.bn, cfg[3] = t.stages;
+    cfg[0] = 2, cfg[1] = p.n1, cfg[2] = t.bm, cfg[3] = t.stages;
   }
   return INT8MM_OK;
 }

@@ -445,6 +445,7 @@ static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st
 template <int T>
 static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipStream_t st) {
   switch (cfg) {
+    case kTile64x128: return run_gemm<T, 64, 128, 1, 4, 3>(c, nbase, nend, st);
     case kTile128Deep: return run_gemm<T, 128, 128, 2, 4, 4>(c, nbase, nend, st);
     case kTile128: return run_gemm<T, 128, 128, 2, 2, 2>(c, nbase, nend, st);
     case kTile256x128: return run_gemm<T, 256, 128, 4, 2, 3>(c, nbase, nend, st);
@@ -461,17 +462,20 @@ static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipS
 //   128x128  0.74 per round of two workgroups per CU (512x5120x20480: 62.0 /
 //            80.1 / 74.4); a last round of at most one per CU takes 0.42,
 //            in the form with four stages and eight wavefronts
-//            (256x5120x5120: 52.9 / 33.4 / 23.0, with two stages and four
-//            wavefronts 25.8);
+//            (512x5120x5120: 52.9 / 34.5 / 23.5, with two stages and four
+//            wavefronts 26.2);
+//   64x128   0.32 on at most 5/8 of the CUs (256x5120x5120: 18.4 us against
+//            22.9 of 128x128), 0.41 on more (128x12288x12288: 55.6, 256x256
+//            134.9), with two per CU it loses (512x5120x5120: 25.6);
 //   decode   0.030 per block of 16 features or tokens that the most loaded CU
 //            reads per K block (77x5136x20464: 29.0 us against 30.1 of 128x128
-//            tiles, 128x5120x5120: 17.8 against 22.4, 128x12288x49152: 161
-//            against 144).
+//            tiles, 128x5120x5120: 17.8 against 22.4, 128x12288x12288: 46.8
+//            against 55.6, 128x12288x49152: 161 against 144).
 // When 256x256 tiles would leave the last round partly empty, the features
 // can be split: [0, n1) in whole rounds of 256x256 tiles, [n1, N) in a second
 // launch of smaller tiles (kGap for its fill and drain, taken when it saves
 // more than kMargin).
-constexpr double kF128 = 0.74, kF128Deep = 0.42, kF256x128 = 0.70, kFDecode = 0.030, kGap = 0.04,
+constexpr double kF128 = 0.74, kF128Deep = 0.42, kF64 = 0.32, kF64More = 0.41, kF256x128 = 0.70, kFDecode = 0.030, kGap = 0.04,
                  kMargin = 0.05;
 
 // The cheapest single launch over n features; ties keep the larger tile.
@@ -490,6 +494,12 @@ static int cheapest_tile(long M, long n, long cus, double* cost) {
   if (c2 < *cost) {
     best = t128 <= cus ? kTile128Deep : kTile128;
     *cost = c2;
+  }
+  const long t64 = (M + 63) / 64 * ((n + 127) / 128);
+  const double c3 = 8 * t64 <= 5 * cus ? kF64 : kF64More;
+  if (t64 <= cus && c3 < *cost) {
+    best = kTile64x128;
+    *cost = c3;
   }
   return best;
 }

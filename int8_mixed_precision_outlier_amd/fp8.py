@@ -218,8 +218,8 @@ def fp8_matmul(X_f8: torch.Tensor, x_scale: torch.Tensor, W_f8: torch.Tensor,
 def fp8_matmul_config(M: int, N: int, K: int):
     """What fp8_matmul launches for these sizes on the current device:
     ("decode", feature blocks of 16 per workgroup, token blocks of 16),
-    ("tiled", BM, BN, stages), or ("split", n1, BN, stages): features below n1
-    in 256x256 tiles, the rest in a second launch of smaller ones."""
+    ("tiled", BM, BN, stages), or ("split", n1, BM, stages): features below n1
+    in 256x256 tiles, the rest in a second launch of BM x 128 tiles."""
     cfg = (ctypes.c_int32 * 4)()
     _check(load().fp8_matmul_config(M, N, K, cfg))
     if cfg[0] == 0:

@@ -245,16 +245,17 @@ def test_matmul(M, K, N, dtype):
         check_product(Y, want, K, dtype, (M, K, N, bias is not None))
 
 
-# the smallest features at which the planner takes each count of feature
-# blocks per workgroup, with an odd last workgroup, on 256 CUs
-DECODE_N = {1: 4080, 2: 4112, 3: 8208, 4: 12304, 5: 16416, 6: 20528, 9: 32800}
+# features at which the planner takes each count of feature blocks per
+# workgroup on 256 CUs, most with a partial last workgroup
+DECODE_N = {1: 4080, 2: 4112, 3: 10272, 4: 12304, 5: 16416, 6: 20528, 9: 32800}
 DECODE_CASES = [(M, R) for M in (1, 9, 16, 17, 32, 33, 48, 50, 64, 70, 96, 97, 128) for R in DECODE_N
-                if R <= (4 if M == 1 else 9 if M <= 64 else 5)]
+                if (R <= 4 if M == 1 else M <= 64 or R <= 5)]
 # (M, N) that take each tile, and the split launch, with ragged last tiles
 TILE_CASES = {(130, 40000): ("tiled", 256, 256, 2), (300, 16368): ("tiled", 256, 128, 3),
-              (100, 40016): ("tiled", 128, 128, 2), (200, 2064): ("tiled", 128, 128, 4),
-              (1100, 20000): ("split", 13056, 128, 2), (2048, 20464): ("split", 16384, 128, 3),
-              (1300, 11952): ("split", 10752, 128, 4)}
+              (100, 40016): ("tiled", 128, 128, 2), (730, 4208): ("tiled", 128, 128, 4),
+              (200, 2064): ("tiled", 64, 128, 3), (530, 32720): ("split", 21760, 128, 2),
+              (2048, 20464): ("split", 16384, 256, 3), (1830, 25808): ("split", 24576, 128, 4),
+              (1300, 11952): ("split", 10752, 64, 3)}
 
 
 @pytest.mark.parametrize("M,R", DECODE_CASES)
@@ -284,8 +285,8 @@ def test_matmul_every_tile(M, N, K):
     xs = torch.rand((kb, M), generator=g, device="cuda") * 2e-3
     ws = torch.rand((nb, kb), generator=g, device="cuda") * 2e-4
     Y = i8.fp8_matmul(xq.view(E4M3), xs, i8.fp8_pack_weight(wq.view(E4M3)), ws, out_dtype=torch.float16)
-    # all rows against a third of the features, the first and the last among them
-    n = np.unique(np.r_[0:N:3, 0:32, N - 32:N, 10740:10770, 13040:13070, 16370:16400])
+    # all rows against a fifth of the features, the first and the last among them
+    n = np.unique(np.r_[0:N:5, 0:32, N - 32:N, 10740:10770, 16370:16400, 21750:21780, 24560:24590])
     n = n[n < N]
     x, w = raw(xq), raw(wq[torch.from_numpy(n).cuda()])
     sw = ws.cpu().numpy()[n // 128]  # a scale per feature: one "block" each
