@@ -32,13 +32,13 @@ namespace {
 constexpr int kMaxKB = 65536 / kFp8Block;
 
 // LDS of a tile: S stages of one K block each (W's half blocks, then X's
-// rows), the token scales [stage][wavefront][its tokens], the tile's weight
-// scales [128-feature block][KB + S], and its bias in fp32.
-template <int BM, int BN, int WM, int WN, int S>
+// rows), the token scales [stage][wavefront][its tokens] (PW > 0: [stage][the
+// tile's tokens]), the tile's weight scales [128-feature block][KB + S], and its bias in fp32.
+template <int BM, int BN, int WM, int WN, int S, int PW>
 struct GemmLds {
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int SX = S * STAGE;
-  static constexpr int SB = SX + S * WN * BM * 4;
+  static constexpr int SB = SX + S * (PW > 0 ? 1 : WN) * BM * 4;
   static constexpr int SW = SB + BN * 4;
   static constexpr int NBT = BN > 128 ? BN / 128 : 1;
   static constexpr int MAX = SW + NBT * (kMaxKB + S) * 4;
@@ -89,19 +89,27 @@ __device__ __forceinline__ void store32(const v4f& ya, const v4f& yb, int nb, in
 
 }  // namespace
 
-template <int T, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
+template <int T, int BM, int BN, int WM, int WN, int S, int PW>
+__global__ __launch_bounds__((WM * WN + PW) * 64, 2) void k_fp8_gemm(
     const uint8_t* __restrict__ X, const float* __restrict__ xs, const uint8_t* __restrict__ W,
     const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y,
     int M, int N, int K, int KB, int tilesM, int tilesN, int groupM, int nbase) {
-  using L = GemmLds<BM, BN, WM, WN, S>;
+  using L = GemmLds<BM, BN, WM, WN, S, PW>;
   constexpr int NWAVE = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int FM = WTM / 16, FN = WTN / 16;
   // 1 KB DMAs of a wavefront per K block: of X, of either half of W, and of
   // its token scales
-  constexpr int XDMA = BM / 8 / NWAVE, HDMA = BN / 16 / NWAVE, SDMA = WTM / 64;
-  static_assert(BN / 16 % NWAVE == 0 && BM / 8 % NWAVE == 0 && WTM % 64 == 0, "DMA split");
+  // PW > 0: the last PW wavefronts only issue the DMAs, the others compute.  A
+  // wavefront that issues waits for the address unit, 16 cycles per DMA; where
+  // one wavefront per SIMD computes, nothing else would use that time
+  // (256x5120x5120 on 64x128 tiles: 18.4 us with the DMAs in the computing
+  // wavefronts, 16.0 with four more; 1024x4096x4096 on 128x128 tiles: 21.4 in
+  // eight computing ones, 19.2 in four more beside four).
+  constexpr int DW = PW > 0 ? PW : NWAVE;  // wavefronts that share the DMAs
+  constexpr int XDMA = BM / 8 / DW, HDMA = BN / 16 / DW, SDMA = PW > 0 ? 1 : WTM / 64;
+  static_assert(BN / 16 % DW == 0 && BM / 8 % DW == 0 && WTM % 64 == 0, "DMA split");
+  constexpr int SROW = PW > 0 ? BM : NWAVE * WTM;  // token scales of a stage
   static_assert(128 % WTN == 0 && FN % 2 == 0 && FM >= 4, "a wavefront's features share a scale block");
   extern __shared__ __align__(16) int8_t smem[];
 
@@ -119,6 +127,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wn = w % WN, wm = w / WN;
+  const int dw = PW > 0 ? max(w - NWAVE, 0) : w;
   const int nrb = N >> 4;
   const int q4 = lane >> 4, r16 = lane & 15;
 
@@ -148,20 +157,25 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   int wdst[2][HDMA];
 #pragma unroll
   for (int j = 0; j < XDMA; ++j) {
-    const int row = min(m0 + (w * XDMA + j) * 8 + xrow, M - 1);
+    const int row = min(m0 + (dw * XDMA + j) * 8 + xrow, M - 1);
     xsrc[j] = (uint32_t)row * (uint32_t)K + chunk * 16u;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int j = 0; j < HDMA; ++j) {
-      const int q = w * HDMA + j;  // half block q % 2 of the half's feature block q / 2
+      const int q = dw * HDMA + j;  // half block q % 2 of the half's feature block q / 2
       const int a = q / 2, fb = a / (FN / 2) * FN + a % (FN / 2) + h * (FN / 2);
       const int rb = min(n0 / 16 + fb, nrb - 1);
       wsrc[h][j] = __builtin_amdgcn_readfirstlane((uint32_t)rb * (uint32_t)KB * 2048u + (q & 1) * 1024u);
       wdst[h][j] = __builtin_amdgcn_readfirstlane(fb * 2048 + (q & 1) * 1024);
     }
-  const int mw = min(m0 + wm * WTM, M - 1);
+  // the tokens whose scales it loads, and their place in a stage: its own, or
+  // 64 of the tile's (some twice, where PW * 64 exceeds them)
+  constexpr int STOK = SDMA * 64;
+  const int stok = PW > 0 ? dw % (BM / 64) * 64 : wm * WTM;
+  const int sdst = PW > 0 ? stok : w * WTM;
+  const int mw = min(m0 + stok, M - 1);
   const uint32_t wbytes = (uint32_t)nrb * (uint32_t)KB * 2048u;
   const uint32_t xbytes = (uint32_t)M * (uint32_t)K;
 
@@ -190,18 +204,18 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
         (void*)X, (short)0, live ? (int)xbytes : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(xs + (size_t)k * M + mw), (short)0, live ? min(M - mw, WTM) * 4 : 0, 0x00020000);
+        (void*)(xs + (size_t)k * M + mw), (short)0, live ? min(M - mw, STOK) * 4 : 0, 0x00020000);
     const bool out = (uint32_t)k * 128u + chunk * 16u >= (uint32_t)K;
 #pragma unroll
     for (int d = d0; d < d1; ++d) {
       if (d < XDMA) {
-        dma16(rx, smem + stage * L::STAGE + BN * 128 + (w * XDMA + d) * 1024,
+        dma16(rx, smem + stage * L::STAGE + BN * 128 + (dw * XDMA + d) * 1024,
               (int)(out ? kOutOfRange : xsrc[d]), k * 128);
       } else if (d < XDMA + HDMA) {
         dma_w(kb, stage, 0, d - XDMA);
       } else {
         const int j = d - XDMA - HDMA;
-        dma4(rs, smem + L::SX + ((stage * NWAVE + w) * WTM + j * 64) * 4, lane * 4 + j * 256, 0);
+        dma4(rs, smem + L::SX + (stage * SROW + sdst + j * 64) * 4, lane * 4 + j * 256, 0);
       }
     }
   };
@@ -212,7 +226,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   };
 
   constexpr bool DB = S > 2;  // two K blocks' fragments in registers
-  static_assert(DB ? FN <= 4 : FN % 4 == 0, "registers; whole halves of W");
+  static_assert(DB ? FN <= 4 : FN % 4 == 0 && PW == 0, "registers; whole halves of W");
   v4f acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
@@ -253,14 +267,16 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
     return join(*reinterpret_cast<const v4i*>(smem + lo + j * 2048),
                 *reinterpret_cast<const v4i*>(smem + hi + j * 2048));
   };
-  const float* sbase = reinterpret_cast<const float*>(smem + L::SX) + w * WTM + r16;
+  const float* sbase =
+      reinterpret_cast<const float*>(smem + L::SX) + (PW > 0 ? wm : w) * WTM + r16;
   auto read_s = [&](int stage, int kb, float(&sx)[FM], float& s_w) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) sx[j] = sbase[stage * NWAVE * WTM + j * 16];
+    for (int j = 0; j < FM; ++j) sx[j] = sbase[stage * SROW + j * 16];
     s_w = my_sw[kb];
   };
 
-  if (KB > 0) {
+  const bool issues = PW == 0 || w >= NWAVE;
+  if (KB > 0 && issues) {
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       dma_a(k, k, 0, OPA);
@@ -269,7 +285,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
   }
   if (t < BN) sb[t] = to_f32<T>(bias_first);
   if (KB > 0)
-    for (int i = t; i < L::NBT * KS; i += NWAVE * 64) sw[i] = i == t ? sw_first : weight_scale(i);
+    for (int i = t; i < L::NBT * KS; i += (NWAVE + PW) * 64) sw[i] = i == t ? sw_first : weight_scale(i);
 
   if constexpr (DB) {
     // 64 x 64 per wavefront: the registers hold all fragments of two K blocks.
@@ -284,6 +300,24 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
       else if (f <= FM) gx[f - 1] = read_x(base + xlo, base + xhi, f - 1);
       else gw[f - FM] = read_w(base + wo, f - FM);
     };
+    if (PW > 0 && w >= NWAVE) {
+      // a wavefront that only issues: the same barriers as the others
+      if (KB > 0) {
+        barrier_vm<(S - 1) * OPS>();
+        barrier_vm<(S - 2) * OPS>();
+        int st = 0;
+        for (int kb = 0; kb < (KB + 1) / 2 * 2; ++kb) {
+          dma_a(kb + S, st, 0, OPA);
+          dma_b(kb + S, st, 0, OPB);
+          barrier_vm<(S - 2) * OPS>();
+          st = st + 1 == S ? 0 : st + 1;
+        }
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no DMA may still write LDS
+      } else {
+        __syncthreads();  // the bias
+      }
+      return;
+    }
     if (KB > 0) {
       barrier_vm<(S - 1) * OPS>();  // the weight scales, and K block 0
 #pragma unroll
@@ -305,9 +339,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
           if (j < R) read(sn, i * R + j, fw[c ^ 1], fx[c ^ 1]);
         }
         if constexpr (i == FN - 1) read_s(sn, kb + 1, sx[c ^ 1], s_w[c ^ 1]);
+        if constexpr (PW == 0) {
 #pragma unroll
-        for (int d = d0; d < d1; ++d) dma_one(kb + S, st, d);
-        order<FM, 2, (R > 2 ? 2 : 1), d1 - d0>();
+          for (int d = d0; d < d1; ++d) dma_one(kb + S, st, d);
+        }
+        order<FM, 2, (R > 2 ? 2 : 1), (PW == 0 ? d1 - d0 : 0)>();
       };
       unroll(block, std::make_integer_sequence<int, FN>{});
       // every wavefront holds K block kb + 1, whose stage may be overwritten,
@@ -416,13 +452,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_fp8_gemm(
 
 // One launch over the features [nbase, nend); nend is N, or a multiple of BN
 // above nbase.
-template <int T, int BM, int BN, int WM, int WN, int S>
+template <int T, int BM, int BN, int WM, int WN, int S, int PW = 0>
 static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st) {
-  using L = GemmLds<BM, BN, WM, WN, S>;
+  using L = GemmLds<BM, BN, WM, WN, S, PW>;
   const int KB = (c.K + kFp8Block - 1) / kFp8Block;
   const int shm = L::SW + L::NBT * (KB + S) * 4;
   const int tilesM = (c.M + BM - 1) / BM, tilesN = (nend - nbase + BN - 1) / BN;
-  auto kern = k_fp8_gemm<T, BM, BN, WM, WN, S>;
+  auto kern = k_fp8_gemm<T, BM, BN, WM, WN, S, PW>;
   // the dynamic-LDS limit is raised once per device the kernels run on
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
@@ -437,7 +473,7 @@ static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st
   // groups of 4 token tiles: the 32 tiles an XCD runs at once share 4 token
   // and 8 feature panels in its L2 (4096x12288x49152: 1963 us; 2 tiles 2035,
   // 8 tiles 1975, 16 tiles 2040)
-  kern<<<tilesM * tilesN, WM * WN * 64, shm, st>>>(c.X, c.xs, c.W, c.ws, c.bias, c.Y, c.M, c.N, c.K,
+  kern<<<tilesM * tilesN, (WM * WN + PW) * 64, shm, st>>>(c.X, c.xs, c.W, c.ws, c.bias, c.Y, c.M, c.N, c.K,
                                                    KB, tilesM, tilesN, tilesM < 4 ? tilesM : 4, nbase);
   return hipGetLastError();
 }
@@ -445,8 +481,8 @@ static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st
 template <int T>
 static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipStream_t st) {
   switch (cfg) {
-    case kTile64x128: return run_gemm<T, 64, 128, 1, 4, 3>(c, nbase, nend, st);
-    case kTile128Deep: return run_gemm<T, 128, 128, 2, 4, 4>(c, nbase, nend, st);
+    case kTile64x128: return run_gemm<T, 64, 128, 1, 4, 3, 4>(c, nbase, nend, st);
+    case kTile128Deep: return run_gemm<T, 128, 128, 2, 2, 4, 4>(c, nbase, nend, st);
     case kTile128: return run_gemm<T, 128, 128, 2, 2, 2>(c, nbase, nend, st);
     case kTile256x128: return run_gemm<T, 256, 128, 4, 2, 3>(c, nbase, nend, st);
     default: return run_gemm<T, 256, 256, 4, 2, 2>(c, nbase, nend, st);
@@ -460,22 +496,22 @@ static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipS
 //   256x128  0.70 per round (one workgroup per CU; 2048x4096x4096: 46.4 /
 //            35.9 / 37.2);
 //   128x128  0.74 per round of two workgroups per CU (512x5120x20480: 62.0 /
-//            80.1 / 74.4); a last round of at most one per CU takes 0.42,
-//            in the form with four stages and eight wavefronts
-//            (512x5120x5120: 52.9 / 34.5 / 23.5, with two stages and four
-//            wavefronts 26.2);
-//   64x128   0.32 on at most 5/8 of the CUs (256x5120x5120: 18.4 us against
-//            22.9 of 128x128), 0.41 on more (128x12288x12288: 55.6, 256x256
-//            134.9), with two per CU it loses (512x5120x5120: 25.6);
-//   decode   0.030 per block of 16 features or tokens that the most loaded CU
-//            reads per K block (77x5136x20464: 29.0 us against 30.1 of 128x128
-//            tiles, 128x5120x5120: 17.8 against 22.4, 128x12288x12288: 46.8
-//            against 55.6, 128x12288x49152: 161 against 144).
+//            80.1 / 74.4); a last round of at most one per CU takes 0.40, in
+//            the form with four stages (512x5120x5120: 52.9 / 34.5 / 20.7, with
+//            two stages 26.2; 256x12288x12288: 134.9 / 91.4 / 64.3);
+//   64x128   0.28 on at most 5/8 of the CUs (256x5120x5120: 16.4 us against
+//            20.3 of 128x128), 0.41 on more (128x12288x12288: 55.6, 256x256
+//            134.9), with two per CU it loses (512x5120x5120: 29.2);
+//   decode   0.031 per block of 16 features or tokens that the most loaded CU
+//            reads per K block (80x5120x5120: 13.1 us; 77x5136x20464: 30.7
+//            against 33.2 on 128x128 tiles; 128x12288x12288: 46.8 against 55.6;
+//            128x5120x5120: 17.8 against 15.8 on 64x128 tiles; 128x12288x49152:
+//            161 against 144).
 // When 256x256 tiles would leave the last round partly empty, the features
 // can be split: [0, n1) in whole rounds of 256x256 tiles, [n1, N) in a second
 // launch of smaller tiles (kGap for its fill and drain, taken when it saves
 // more than kMargin).
-constexpr double kF128 = 0.74, kF128Deep = 0.42, kF64 = 0.32, kF64More = 0.41, kF256x128 = 0.70, kFDecode = 0.030, kGap = 0.04,
+constexpr double kF128 = 0.74, kF128Deep = 0.40, kF64 = 0.28, kF64More = 0.41, kF256x128 = 0.70, kFDecode = 0.031, kGap = 0.04,
                  kMargin = 0.05;
 
 // The cheapest single launch over n features; ties keep the larger tile.
