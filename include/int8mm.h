@@ -459,7 +459,7 @@ int fp8_matmul(const void *X_f8, const float *x_scale, int64_t M, int64_t K,
  * host only, as int8mm_kernel_config.  cfg[4]:
  *   weight-streaming kernel (M <= 64, and up to 128 where it is faster than
  *     the tiles): {0, blocks of 16 features per workgroup (1-6, 9), blocks of
- *     16 tokens (1-4, 6, 8), 0};
+ *     16 tokens (1-8), 0};
  *   tiles: {1, tile rows, tile columns, LDS stages};
  *   tiles in two launches: {2, n1, tile rows, LDS stages of the second}:
  *     features [0, n1) in 256x256 tiles, [n1, N) in smaller ones of 128 columns.

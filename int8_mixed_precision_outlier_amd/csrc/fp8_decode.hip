@@ -220,13 +220,6 @@ static hipError_t run_decode(const Fp8Call& c, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Token blocks of the kernel that M tokens take: as many as they need up to
-// 4, then 6 or 8.
-static int token_blocks(int M) {
-  const int T = (M + 15) / 16;
-  return T <= 4 ? T : (T + 1) / 2 * 2;
-}
-
 // Feature blocks per workgroup.  A CU takes in a bounded rate of operands, so
 // the time goes with the most loaded CU's rounds of workgroups times the
 // blocks it reads per K block in each, R of the weight and T of the tokens;
@@ -238,15 +231,15 @@ static int token_blocks(int M) {
 // with four or more blocks per CU one block per workgroup is best, the most
 // loads in flight (1x12288x36864, R = 1, 3, 9: 65.4, 68.3, 69.9).  Above 64
 // tokens the partial sums of more than 5 blocks would not fit LDS, and above
-// 96 the sizes where 2 or 5 would be best run faster on tiles.
+// 112 the sizes where 2 or 5 would be best run faster on tiles.
 constexpr int kDecodeR[] = {1, 2, 3, 4, 5, 6, 9};
 
 Fp8DecodePlan fp8_decode_plan(int M, int N) {
-  const int cus = device_cu_count(), nrb = N / 16, T = token_blocks(M);
+  const int cus = device_cu_count(), nrb = N / 16, T = (M + 15) / 16;
   Fp8DecodePlan best{1, T, INT64_MAX};
   for (int R : kDecodeR) {
     if (T > 4 && R > 5) break;
-    if (T > 6 && (R == 2 || R == 5)) continue;
+    if (T > 7 && (R == 2 || R == 5)) continue;
     const int64_t groups = (nrb + R - 1) / R, cost = (groups + cus - 1) / cus * (R + T);
     if (cost < best.cost) best = Fp8DecodePlan{R, T, cost};
     if (M <= 8 && nrb >= 4 * cus) break;
@@ -265,7 +258,7 @@ static hipError_t decode_blocks(int R, const Fp8Call& c, hipStream_t st) {
     case 3: return run_decode<TY, 3, T, KS, 1>(c, st);
     case 4: return run_decode<TY, 4, T, 4, 1>(c, st);
   }
-  if constexpr (T <= 6) {
+  if constexpr (T <= 7) {
     if (R == 2) return run_decode<TY, 2, T, KS, 1>(c, st);
     if (R == 5) return run_decode<TY, 5, T, 4, 1>(c, st);
   }
@@ -282,7 +275,9 @@ static hipError_t decode_tokens(const Fp8Call& c, hipStream_t st) {
     case 2: return decode_blocks<TY, 2>(p.R, c, st);
     case 3: return decode_blocks<TY, 3>(p.R, c, st);
     case 4: return decode_blocks<TY, 4>(p.R, c, st);
+    case 5: return decode_blocks<TY, 5>(p.R, c, st);
     case 6: return decode_blocks<TY, 6>(p.R, c, st);
+    case 7: return decode_blocks<TY, 7>(p.R, c, st);
     default: return decode_blocks<TY, 8>(p.R, c, st);
   }
 }

@@ -184,7 +184,7 @@ def test_kernel_choice_over_seeded_sizes():
         if M <= 64 or c[0] == "decode":
             T = -(-M // 16)
             assert c[0] == "decode" and M <= 128 and c[1] in (1, 2, 3, 4, 5, 6, 9), (M, N, c)
-            assert c[2] == (T if T <= 4 else T + T % 2) and (T <= 4 or c[1] in ((1, 2, 3, 4, 5), (1, 3, 4))[T > 6]), (M, N, c)
+            assert c[2] == T and (T <= 4 or c[1] in ((1, 2, 3, 4, 5), (1, 3, 4))[T > 7]), (M, N, c)
         elif c[0] == "tiled":
             assert c[1:] in tiles, (M, N, c)
         else:

@@ -248,8 +248,9 @@ def test_matmul(M, K, N, dtype):
 # features at which the planner takes each count of feature blocks per
 # workgroup on 256 CUs, most with a partial last workgroup
 DECODE_N = {1: 4080, 2: 4112, 3: 10272, 4: 12304, 5: 16416, 6: 20528, 9: 32800}
-DECODE_CASES = [(M, R) for M in (1, 9, 16, 17, 32, 33, 48, 50, 64, 70, 96, 97, 128) for R in DECODE_N
-                if (R <= 4 if M == 1 else M <= 64 or R <= 5) and not (M > 96 and R in (2, 5))]
+DECODE_CASES = [(M, R) for M in (1, 9, 16, 17, 32, 33, 48, 50, 64, 70, 96, 97, 112, 128)
+                for R in DECODE_N
+                if (R <= 4 if M == 1 else M <= 64 or R <= 5) and not (M > 112 and R in (2, 5))]
 # (M, N) that take each tile, and the split launch, with ragged last tiles
 TILE_CASES = {(130, 40000): ("tiled", 256, 256, 2), (300, 16368): ("tiled", 256, 128, 3),
               (100, 40016): ("tiled", 128, 128, 2), (730, 4208): ("tiled", 128, 128, 4),
@@ -262,8 +263,8 @@ TILE_CASES = {(130, 40000): ("tiled", 256, 256, 2), (300, 16368): ("tiled", 256,
 def test_matmul_every_streaming_kernel(M, R):
     """Every (feature blocks, token blocks) of the weight-streaming kernel, with
     fewer K blocks than wavefronts and, for the small ones, more."""
-    N, T = DECODE_N[R], -(-M // 16)
-    assert i8.fp8_matmul_config(M, N, 272) == ("decode", R, T if T <= 4 else T + T % 2)
+    N = DECODE_N[R]
+    assert i8.fp8_matmul_config(M, N, 272) == ("decode", R, -(-M // 16))
     for K in (272, 2192) if R <= 2 else (272,):
         xq, xs, wq, ws = operands(M, K, N, M + R)
         b = torch.randn(N, generator=torch.Generator().manual_seed(N)).to(torch.bfloat16)
