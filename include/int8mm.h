@@ -370,9 +370,10 @@ int int8mm_kernel_config(int64_t M, int64_t N, int64_t K, int32_t *cfg);
  *   - Inputs need not be finite: a NaN or an infinity leaves as NaN (an
  *     infinity also makes its block's scale infinite), and the products
  *     that meet it are NaN.
- *   - Everything runs in one launch (or several in a row for more than 2^20
- *     rows) on `stream`, without a workspace; results do not depend on
- *     timing, and calls on different streams may overlap.
+ *   - Outputs do not overlap inputs, but for fp8_rms_norm's H as stated there.
+ *   - Everything runs in one launch (two for some products, several in a row
+ *     for more than 2^20 rows) on `stream`, without a workspace; results do
+ *     not depend on timing, and calls on different streams may overlap.
  */
 typedef enum { INT8MM_F16 = 0, INT8MM_BF16 = 1 } int8mm_type;
 
@@ -421,7 +422,8 @@ int fp8_quantize(const void *X, int type, int64_t M, int64_t K, void *X_f8,
  *   eps          in  > 0, finite.
  *   H            out [M][K], the new residual h; NULL if and only if
  *                    residual is.  May be the residual's or X's own buffer.
- * Sums are held in fp32.
+ * Sums are held in fp32: a row of bf16 magnitudes near 2^64 overflows its sum
+ * of squares, and y is then 0.
  */
 int fp8_rms_norm(const void *X, const void *residual, const void *weight,
                  int type, int64_t M, int64_t K, float eps, void *H,

@@ -349,6 +349,11 @@ def test_empty_sizes():
     Y = i8.fp8_matmul(e(3, 0), e(0, 3, d=f), e(32, 0), e(1, 0, d=f), bias=b)
     assert torch.equal(Y, b.expand(3, 32))
     assert not i8.fp8_matmul(e(3, 0), e(0, 3, d=f), e(32, 0), e(1, 0, d=f)).any()
+    for (M, N) in TILE_CASES:  # K = 0 on every tile
+        b = torch.arange(N, device="cuda").remainder(251).to(torch.bfloat16)
+        Y = i8.fp8_matmul(e(M, 0), e(0, M, d=f), e(N, 0), e(-(-N // 128), 0, d=f), bias=b)
+        assert torch.equal(Y, b.expand(M, N)), (M, N)
+    b = torch.arange(32, dtype=torch.bfloat16, device="cuda")
     assert i8.fp8_matmul(e(0, 128), e(1, 0, d=f), e(32, 128), e(1, 1, d=f)).shape == (0, 32)
     assert i8.fp8_matmul(e(3, 128), e(1, 3, d=f), e(0, 128), e(0, 1, d=f)).shape == (3, 0)
     q, s = i8.fp8_quantize(e(0, 256, d=torch.float16))
@@ -520,6 +525,57 @@ def test_results_do_not_change_between_runs():
     args = on_gpu(xq, xs, wq, ws)
     first = i8.fp8_matmul(*args)
     assert all(torch.equal(i8.fp8_matmul(*args), first) for _ in range(5))
+
+
+@pytest.mark.parametrize("M,N", [(40, 2064), (64, 36880), (200, 2064), (730, 4208), (300, 16368), (530, 32720)])
+def test_matmul_leaves_memory_behind_y(M, N):
+    """Y inside a larger buffer: nothing is written in front of it or behind."""
+    K = 144
+    xq, xs, wq, ws = operands(M, K, N, 3)
+    args = on_gpu(xq, xs, wq, ws)
+    buf = torch.full((M * N + 4096,), 5.0, dtype=torch.bfloat16, device="cuda")
+    Y = buf[2048: 2048 + M * N].view(M, N)
+    i8.fp8_matmul(*args, out=Y)
+    assert bool((buf[:2048] == 5).all()) and bool((buf[2048 + M * N:] == 5).all())
+    assert torch.equal(Y, i8.fp8_matmul(*args))
+
+
+@pytest.mark.parametrize("M,K", [(1, 144), (17, 1040), (600, 272), (3, 12304)])
+def test_row_operators_leave_memory_behind(M, K):
+    X = acts(M, 2 * K, torch.bfloat16, 1)
+    kb = -(-K // 128)
+    q = torch.full((M * K + 512,), 1.0, device="cuda").to(E4M3)
+    s = torch.full((kb * M + 64,), 7.0, device="cuda")
+    out = (q[256: 256 + M * K].view(M, K), s[32: 32 + kb * M].view(kb, M))
+    x = X[:, :K].contiguous()
+    H = torch.full((M * K + 64,), 9.0, dtype=torch.bfloat16, device="cuda")
+    g = x[0].contiguous()
+    for call in (lambda: i8.fp8_quantize(x, out=out), lambda: i8.fp8_silu_mul(X, out=out),
+                 lambda: i8.fp8_rms_norm(x, g, residual=x, residual_out=H[32: 32 + M * K].view(M, K), out=out)):
+        call()
+        assert bool((q[:256].float() == 1).all()) and bool((q[256 + M * K:].float() == 1).all())
+        assert bool((s[:32] == 7).all()) and bool((s[32 + kb * M:] == 7).all())
+    assert bool((H[:32] == 9).all()) and bool((H[32 + M * K:] == 9).all())
+
+
+def test_first_call_inside_a_capture():
+    """Sizes whose kernels have not run in this process, captured at once: every
+    replay gives what an eager call gives afterwards."""
+    M, K, N = 1900, 272, 9600
+    assert i8.fp8_matmul_config(M, N, K)[0] == "split"
+    x, w = codes(M * K, 1).view(M, K).view(E4M3), codes(N * K, 2).view(N, K).view(E4M3)
+    xs = torch.rand((3, M), device="cuda") * 1e-3
+    ws = torch.rand((75, 3), device="cuda") * 1e-3
+    wp = i8.fp8_pack_weight(w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y = i8.fp8_matmul(x, xs, wp, ws)
+    for _ in range(3):
+        Y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, i8.fp8_matmul(x, xs, wp, ws))
 
 
 def codes(n, seed):
