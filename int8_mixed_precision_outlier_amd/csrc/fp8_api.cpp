@@ -122,7 +122,7 @@ int fp8_matmul_config(int64_t M, int64_t N, int64_t K, int32_t* cfg) {
     int32_t bm, bn, stages;
   };
   static constexpr Tile kTiles[] = {{256, 256, 2}, {256, 128, 3}, {128, 128, 2}, {128, 128, 4},
-                                    {64, 128, 3}};
+                                    {64, 128, 4}};
   const Fp8Plan p = fp8_plan((int)M, (int)N);
   if (p.first == kDecode) {
     const Fp8DecodePlan d = fp8_decode_plan((int)M, (int)N);

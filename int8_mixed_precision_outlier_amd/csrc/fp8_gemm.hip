@@ -104,7 +104,7 @@ __global__ __launch_bounds__((WM * WN + PW) * 64, 2) void k_fp8_gemm(
   // wavefront that issues waits for the address unit, 16 cycles per DMA; where
   // one wavefront per SIMD computes, nothing else would use that time
   // (256x5120x5120 on 64x128 tiles: 18.4 us with the DMAs in the computing
-  // wavefronts, 16.0 with four more; 1024x4096x4096 on 128x128 tiles: 21.4 in
+  // wavefronts, 15.8 with four more, both with three stages; 1024x4096x4096 on 128x128 tiles: 21.4 in
   // eight computing ones, 19.2 in four more beside four).
   constexpr int DW = PW > 0 ? PW : NWAVE;  // wavefronts that share the DMAs
   constexpr int XDMA = BM / 8 / DW, HDMA = BN / 16 / DW, SDMA = PW > 0 ? 1 : WTM / 64;
@@ -481,7 +481,7 @@ static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st
 template <int T>
 static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipStream_t st) {
   switch (cfg) {
-    case kTile64x128: return run_gemm<T, 64, 128, 1, 4, 3, 4>(c, nbase, nend, st);
+    case kTile64x128: return run_gemm<T, 64, 128, 1, 4, 4, 4>(c, nbase, nend, st);
     case kTile128Deep: return run_gemm<T, 128, 128, 2, 2, 4, 4>(c, nbase, nend, st);
     case kTile128: return run_gemm<T, 128, 128, 2, 2, 2>(c, nbase, nend, st);
     case kTile256x128: return run_gemm<T, 256, 128, 4, 2, 3>(c, nbase, nend, st);
@@ -499,13 +499,13 @@ static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipS
 //            80.1 / 74.4); a last round of at most one per CU takes 0.40, in
 //            the form with four stages (512x5120x5120: 52.9 / 34.5 / 20.7, with
 //            two stages 26.2; 256x12288x12288: 134.9 / 91.4 / 64.3);
-//   64x128   0.28 on at most 5/8 of the CUs (256x5120x5120: 16.4 us against
-//            20.3 of 128x128), 0.41 on more (128x12288x12288: 55.6, 256x256
-//            134.9), with two per CU it loses (512x5120x5120: 29.2);
+//   64x128   0.28 on at most 5/8 of the CUs (256x5120x5120: 14.7 us against
+//            20.3 of 128x128; 15.8 with three stages), 0.41 on more
+//            (128x12288x12288: 49.7, 256x256 134.9), with two per CU it loses (512x5120x5120: 29.2);
 //   decode   0.031 per block of 16 features or tokens that the most loaded CU
 //            reads per K block (80x5120x5120: 13.1 us; 77x5136x20464: 30.7
-//            against 33.2 on 128x128 tiles; 128x12288x12288: 46.8 against 55.6;
-//            128x5120x5120: 17.8 against 15.8 on 64x128 tiles; 128x12288x49152:
+//            against 33.2 on 128x128 tiles; 128x12288x12288: 48.5 against 49.7;
+//            128x5120x5120: 17.8 against 14.3 on 64x128 tiles; 128x12288x49152:
 //            161 against 144).
 // When 256x256 tiles would leave the last round partly empty, the features
 // can be split: [0, n1) in whole rounds of 256x256 tiles, [n1, N) in a second

@@ -174,7 +174,7 @@ def test_kernel_choice_over_seeded_sizes():
     if torch.cuda.is_available() and torch.cuda.get_device_properties(0).multi_processor_count != 256:
         pytest.skip("the expected choices are those of 256 CUs")
     rng = np.random.default_rng(77)
-    tiles = {(256, 256, 2), (256, 128, 3), (128, 128, 2), (128, 128, 4), (64, 128, 3)}
+    tiles = {(256, 256, 2), (256, 128, 3), (128, 128, 2), (128, 128, 4), (64, 128, 4)}
     seen = set()
     for _ in range(4000):
         M = int(rng.choice([rng.integers(1, 129), rng.integers(129, 6000)]))

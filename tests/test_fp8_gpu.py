@@ -254,9 +254,9 @@ DECODE_CASES = [(M, R) for M in (1, 9, 16, 17, 32, 33, 48, 50, 64, 70, 96, 97, 1
 # (M, N) that take each tile, and the split launch, with ragged last tiles
 TILE_CASES = {(130, 40000): ("tiled", 256, 256, 2), (300, 16368): ("tiled", 256, 128, 3),
               (100, 40016): ("tiled", 128, 128, 2), (730, 4208): ("tiled", 128, 128, 4),
-              (200, 2064): ("tiled", 64, 128, 3), (530, 32720): ("split", 21760, 128, 2),
+              (200, 2064): ("tiled", 64, 128, 4), (530, 32720): ("split", 21760, 128, 2),
               (2048, 20464): ("split", 16384, 256, 3), (1830, 25808): ("split", 24576, 128, 4),
-              (1300, 11600): ("split", 10752, 64, 3)}
+              (1300, 11600): ("split", 10752, 64, 4)}
 
 
 @pytest.mark.parametrize("M,R", DECODE_CASES)
