@@ -230,8 +230,10 @@ static hipError_t run_decode(const Fp8Call& c, hipStream_t st) {
 // tokens bring little token traffic (the rows past M repeat the last one):
 // with four or more blocks per CU one block per workgroup is best, the most
 // loads in flight (1x12288x36864, R = 1, 3, 9: 65.4, 68.3, 69.9).  Above 64
-// tokens the partial sums of more than 5 blocks would not fit LDS, and above
-// 112 the sizes where 2 or 5 would be best run faster on tiles.
+// tokens the partial sums of more than 5 blocks would not fit LDS, and where 1
+// to 4 blocks and the tokens' make more than 9, 64x128 tiles are faster
+// (120x5120x16384, 4 blocks: 27.3 us against 23.6), above 112 tokens tiles
+// also where 5 would be best.
 constexpr int kDecodeR[] = {1, 2, 3, 4, 5, 6, 9};
 
 Fp8DecodePlan fp8_decode_plan(int M, int N) {
@@ -239,7 +241,7 @@ Fp8DecodePlan fp8_decode_plan(int M, int N) {
   Fp8DecodePlan best{1, T, INT64_MAX};
   for (int R : kDecodeR) {
     if (T > 4 && R > 5) break;
-    if (T > 7 && (R == 2 || R == 5)) continue;
+    if (T > 4 && (R < 5 ? R + T > 9 : T > 7)) continue;
     const int64_t groups = (nrb + R - 1) / R, cost = (groups + cus - 1) / cus * (R + T);
     if (cost < best.cost) best = Fp8DecodePlan{R, T, cost};
     if (M <= 8 && nrb >= 4 * cus) break;
@@ -253,15 +255,15 @@ Fp8DecodePlan fp8_decode_plan(int M, int N) {
 template <int TY, int T>
 static hipError_t decode_blocks(int R, const Fp8Call& c, hipStream_t st) {
   constexpr int KS = T <= 4 ? 8 : 4;
-  switch (R) {
-    case 1: return run_decode<TY, 1, T, KS, 1>(c, st);
-    case 3: return run_decode<TY, 3, T, KS, 1>(c, st);
-    case 4: return run_decode<TY, 4, T, 4, 1>(c, st);
-  }
+  if (R == 1) return run_decode<TY, 1, T, KS, 1>(c, st);
   if constexpr (T <= 7) {
     if (R == 2) return run_decode<TY, 2, T, KS, 1>(c, st);
     if (R == 5) return run_decode<TY, 5, T, 4, 1>(c, st);
   }
+  if constexpr (T <= 6)
+    if (R == 3) return run_decode<TY, 3, T, KS, 1>(c, st);
+  if constexpr (T <= 5)
+    if (R == 4) return run_decode<TY, 4, T, 4, 1>(c, st);
   if constexpr (T <= 4)
     return R == 6 ? run_decode<TY, 6, T, 4, 1>(c, st) : run_decode<TY, 9, T, 4, 1>(c, st);
   return hipErrorInvalidValue;

@@ -104,8 +104,8 @@ __global__ __launch_bounds__((WM * WN + PW) * 64, 2) void k_fp8_gemm(
   // wavefront that issues waits for the address unit, 16 cycles per DMA; where
   // one wavefront per SIMD computes, nothing else would use that time
   // (256x5120x5120 on 64x128 tiles: 18.4 us with the DMAs in the computing
-  // wavefronts, 15.8 with four more, both with three stages; 1024x4096x4096 on 128x128 tiles: 21.4 in
-  // eight computing ones, 19.2 in four more beside four).
+  // wavefronts, 15.8 with four more, both with three stages; 1024x4096x4096 on
+  // 128x128 tiles: 21.4 in eight computing ones, 19.2 in four more beside four).
   constexpr int DW = PW > 0 ? PW : NWAVE;  // wavefronts that share the DMAs
   constexpr int XDMA = BM / 8 / DW, HDMA = BN / 16 / DW, SDMA = PW > 0 ? 1 : WTM / 64;
   static_assert(BN / 16 % DW == 0 && BM / 8 % DW == 0 && WTM % 64 == 0, "DMA split");
@@ -500,19 +500,22 @@ static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipS
 //            the form with four stages (512x5120x5120: 52.9 / 34.5 / 20.7, with
 //            two stages 26.2; 256x12288x12288: 134.9 / 91.4 / 64.3);
 //   64x128   0.28 on at most 5/8 of the CUs (256x5120x5120: 14.7 us against
-//            20.3 of 128x128; 15.8 with three stages), 0.41 on more
-//            (128x12288x12288: 49.7, 256x256 134.9), with two per CU it loses (512x5120x5120: 29.2);
+//            20.3 of 128x128; 15.8 with three stages), 0.305 on more
+//            (192x5120x10240: 16.0 against 22.2; 256x12288x8192: 46.7 against
+//            59.6), with two per CU it loses (512x5120x5120: 28.8 against 21.5);
 //   decode   0.031 per block of 16 features or tokens that the most loaded CU
-//            reads per K block (80x5120x5120: 13.1 us; 77x5136x20464: 30.7
-//            against 33.2 on 128x128 tiles; 128x12288x12288: 48.5 against 49.7;
-//            128x5120x5120: 17.8 against 14.3 on 64x128 tiles; 128x12288x49152:
-//            161 against 144).
+//            reads per K block (77x5136x20464: 30.7 us against 33.2 on 128x128
+//            tiles; with weights that no cache holds, decode / 64x128 tiles:
+//            104x5120x8192 17.8 / 19.4, 120x5120x5120 22.1 / 20.4, 96x5120x12288
+//            20.1 / 20.7, 120x5120x16384 27.3 / 23.6, but 120x12288x12288 45.2 /
+//            48.9; with weights in the last-level cache 104x5120x12288 22.9 /
+//            15.1; 128x12288x49152: 161 against 144 on 128x128 tiles).
 // When 256x256 tiles would leave the last round partly empty, the features
 // can be split: [0, n1) in whole rounds of 256x256 tiles, [n1, N) in a second
 // launch of smaller tiles (kGap for its fill and drain, taken when it saves
 // more than kMargin).
-constexpr double kF128 = 0.74, kF128Deep = 0.40, kF64 = 0.28, kF64More = 0.41, kF256x128 = 0.70, kFDecode = 0.031, kGap = 0.04,
-                 kMargin = 0.05;
+constexpr double kF128 = 0.74, kF128Deep = 0.40, kF64 = 0.28, kF64More = 0.305,
+                 kF256x128 = 0.70, kFDecode = 0.031, kGap = 0.04, kMargin = 0.05;
 
 // The cheapest single launch over n features; ties keep the larger tile.
 static int cheapest_tile(long M, long n, long cus, double* cost) {

@@ -250,11 +250,13 @@ def test_matmul(M, K, N, dtype):
 DECODE_N = {1: 4080, 2: 4112, 3: 10272, 4: 12304, 5: 16416, 6: 20528, 9: 32800}
 DECODE_CASES = [(M, R) for M in (1, 9, 16, 17, 32, 33, 48, 50, 64, 70, 96, 97, 112, 128)
                 for R in DECODE_N
-                if (R <= 4 if M == 1 else M <= 64 or R <= 5) and not (M > 112 and R in (2, 5))]
+                if (R <= 4 if M == 1 else M <= 64 or (R + -(-M // 16) <= 9 if R < 5 else
+                                                      R == 5 and M <= 112))]
 # (M, N) that take each tile, and the split launch, with ragged last tiles
 TILE_CASES = {(130, 40000): ("tiled", 256, 256, 2), (300, 16368): ("tiled", 256, 128, 3),
               (100, 40016): ("tiled", 128, 128, 2), (730, 4208): ("tiled", 128, 128, 4),
-              (200, 2064): ("tiled", 64, 128, 4), (530, 32720): ("split", 21760, 128, 2),
+              (200, 2064): ("tiled", 64, 128, 4), (300, 6416): ("tiled", 64, 128, 4),
+              (530, 32720): ("split", 21760, 128, 2),
               (2048, 20464): ("split", 16384, 256, 3), (1830, 25808): ("split", 24576, 128, 4),
               (1300, 11600): ("split", 10752, 64, 4)}
 
