@@ -41,16 +41,17 @@ def _blocks(n: int) -> int:
 
 
 def _tensor(t, name: str, dtypes, shape, device=None):
-    """A contiguous GPU tensor of one of `dtypes` and of `shape` (None: any
-    size), on `device` if given."""
+    """A contiguous GPU tensor of one of `dtypes` and of `shape` (its first
+    size None: any), or with `shape` dimensions, on `device` if given."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     have = t.shape
-    if have != shape and (len(have) != len(shape)
-                          or any(w is not None and h != w for h, w in zip(have, shape))):
-        want = tuple("any" if w is None else w for w in shape)
+    if (len(have) != shape if isinstance(shape, int) else
+            have != shape and (len(have) != len(shape) or shape[0] is not None or have[1:] != shape[1:])):
+        want = ((None,) * shape if isinstance(shape, int) else shape)
+        want = tuple("any" if w is None else w for w in want)
         raise ValueError(f"{name} must have shape {want}, got {tuple(have)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -63,11 +64,12 @@ def _tensor(t, name: str, dtypes, shape, device=None):
 # object around it first (3 us of a single-token call's 13)
 _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _elsewhere(t, stream) -> bool:
     """Whether a call on t's device (and `stream`) has to make them current first."""
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+    return stream is not None or t.get_device() != _device_now()
 
 
 @contextlib.contextmanager
@@ -83,10 +85,12 @@ def _at(t):
     return None if t is None else t.data_ptr() or None
 
 
-def _quantized(out, M, K, device):
-    """The (e4m3 [M, K], scales [ceil(K/128), M]) a quantizer writes: `out`, or new."""
+def _quantized(out, M, K, device, like=None):
+    """The (e4m3 [M, K], scales [ceil(K/128), M]) a quantizer writes: `out`, or
+    new (empty_like, where a tensor of that shape is at hand, is the faster call)."""
     if out is None:
-        return (torch.empty((M, K), dtype=_E4M3, device=device),
+        return (torch.empty((M, K), dtype=_E4M3, device=device) if like is None
+                else torch.empty_like(like, dtype=_E4M3),
                 torch.empty((_blocks(K), M), dtype=torch.float32, device=device))
     q, s = out
     return (_tensor(q, "out[0]", (_E4M3,), (M, K), device),
@@ -97,7 +101,7 @@ def fp8_pack_weight(Wq: torch.Tensor, stream=None) -> torch.Tensor:
     """e4m3 weights [N,K] row-major (a checkpoint's, with scales [ceil(N/128),
     ceil(K/128)]) -> the packed layout, as an e4m3 tensor [N, fp8_kpad(K)] (an
     opaque buffer)."""
-    _tensor(Wq, "Wq", (_E4M3,), (None, None))
+    _tensor(Wq, "Wq", (_E4M3,), 2)
     if _elsewhere(Wq, stream):
         with _current(Wq, stream):
             return fp8_pack_weight(Wq)
@@ -110,7 +114,7 @@ def fp8_pack_weight(Wq: torch.Tensor, stream=None) -> torch.Tensor:
 def fp8_quantize_weight(W: torch.Tensor, stream=None):
     """W fp16 or bf16 [K,N] -> (W_f8 packed e4m3 [N, fp8_kpad(K)], w_scale fp32
     [ceil(N/128), ceil(K/128)]), one scale per 128 x 128 block."""
-    _tensor(W, "W", _HALVES, (None, None))
+    _tensor(W, "W", _HALVES, 2)
     if _elsewhere(W, stream):
         with _current(W, stream):
             return fp8_quantize_weight(W)
@@ -125,12 +129,12 @@ def fp8_quantize_weight(W: torch.Tensor, stream=None):
 def fp8_quantize(X: torch.Tensor, out=None, stream=None):
     """X fp16 or bf16 [M,K] -> (X_f8 e4m3 [M,K], x_scale fp32 [ceil(K/128), M]).
     `out`: such a pair to write into."""
-    _tensor(X, "X", _HALVES, (None, None))
+    _tensor(X, "X", _HALVES, 2)
     if _elsewhere(X, stream):
         with _current(X, stream):
             return fp8_quantize(X, out=out)
     M, K = X.shape
-    X_f8, x_scale = _quantized(out, M, K, X.device)
+    X_f8, x_scale = _quantized(out, M, K, X.device, X)
     _check(load().fp8_quantize(_at(X), _TYPES[X.dtype], M, K, _at(X_f8), _at(x_scale),
                                _stream_of(X.get_device())))
     return X_f8, x_scale
@@ -143,7 +147,7 @@ def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     (X_f8, x_scale), or with `residual` [M,K], whose sum with X (rounded to
     their type) is normed instead, (X_f8, x_scale, H) with H that sum.
     `residual_out` takes H; it may be `residual` itself."""
-    _tensor(X, "X", _HALVES, (None, None))
+    _tensor(X, "X", _HALVES, 2)
     if _elsewhere(X, stream):
         with _current(X, stream):
             return fp8_rms_norm(X, weight, eps, residual, residual_out, out)
@@ -155,10 +159,10 @@ def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             _tensor(residual_out, "residual_out", (X.dtype,), (M, K), X.device)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    X_f8, x_scale = _quantized(out, M, K, X.device)
+    X_f8, x_scale = _quantized(out, M, K, X.device, X)
     H = residual_out
     if residual is not None and H is None:
-        H = torch.empty((M, K), dtype=X.dtype, device=X.device)
+        H = torch.empty_like(X)
     _check(load().fp8_rms_norm(_at(X), _at(residual), _at(weight), _TYPES[X.dtype], M, K,
                                float(eps), _at(H), _at(X_f8), _at(x_scale),
                                _stream_of(X.get_device())))
@@ -168,7 +172,7 @@ def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 def fp8_silu_mul(gate_up: torch.Tensor, out=None, stream=None):
     """gate_up fp16 or bf16 [M,2K] (K gates, then K ups) -> the quantized
     silu(gate) * up: (A_f8 e4m3 [M,K], a_scale fp32 [ceil(K/128), M])."""
-    _tensor(gate_up, "gate_up", _HALVES, (None, None))
+    _tensor(gate_up, "gate_up", _HALVES, 2)
     if _elsewhere(gate_up, stream):
         with _current(gate_up, stream):
             return fp8_silu_mul(gate_up, out=out)
@@ -190,7 +194,7 @@ def fp8_matmul(X_f8: torch.Tensor, x_scale: torch.Tensor, W_f8: torch.Tensor,
     [ceil(K/128), M]) and the packed W_f8 [N, fp8_kpad(K)] (with w_scale
     [ceil(N/128), ceil(K/128)]), plus `bias` [N].  Y and bias are of
     `out_dtype` (fp16 or bf16; by default that of `out`, else of bias, else bf16)."""
-    _tensor(X_f8, "X_f8", (_E4M3,), (None, None))
+    _tensor(X_f8, "X_f8", (_E4M3,), 2)
     if _elsewhere(X_f8, stream):
         with _current(X_f8, stream):
             return fp8_matmul(X_f8, x_scale, W_f8, w_scale, bias, out_dtype, out)
