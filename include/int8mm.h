@@ -368,8 +368,8 @@ int int8mm_kernel_config(int64_t M, int64_t N, int64_t K, int32_t *cfg);
  *     scale = RN32(a / 448), q = e4m3_rne(RN32(x * RN32(448 / a))), x ~ q * scale.
  *     fp8_quantize is therefore reproducible bit for bit.
  *   - Inputs need not be finite: a NaN or an infinity leaves as NaN (an
- *     infinity also makes its block's scale infinite), and the products
- *     that meet it are NaN.
+ *     infinity that reaches the quantizer also makes its block's scale
+ *     infinite), and the products that meet it are NaN.
  *   - Outputs do not overlap inputs, but for fp8_rms_norm's H as stated there.
  *   - Everything runs in one launch (two for some products, several in a row
  *     for more than 2^20 rows) on `stream`, without a workspace; results do
@@ -432,7 +432,8 @@ int fp8_rms_norm(const void *X, const void *residual, const void *weight,
 /*
  * fp8_silu_mul -- the gated activation before a feed-forward's second
  * product: gate_up [M][2K] (16-bit; a row is its K gates, then its K ups) ->
- * the quantized g / (1 + exp(-g)) * u, in fp32 up to the quantizer.
+ * the quantized g / (1 + exp(-g)) * u, in fp32 up to the quantizer.  Finite
+ * gates below -87.33, where 1 / (1 + exp(-g)) is no normal fp32 number, give 0.
  * M * 2K <= INT8MM_MAX_MN.
  */
 int fp8_silu_mul(const void *gate_up, int type, int64_t M, int64_t K,

@@ -41,13 +41,18 @@ __device__ __forceinline__ uint2 quant8(const float (&y)[8], float& scale) {
 // its own), so that its error stays at the exponential instruction's, and
 // the quotient is a product with the reciprocal instruction's result: within
 // 8 half steps in all, at a third of the instructions of expf and the IEEE
-// division, which bound this kernel (2048x20480 with two blocks per group: 37.9 us; with expf and four: 50.8).  exp
-// overflows to infinity below g = -88.7, where the quotient is a signed zero,
-// as in the limit.
+// division, which bound this kernel (2048x20480 with two blocks per group:
+// 37.9 us; with expf and four: 50.8).  Below g = -87.33 the reciprocal leaves
+// the normal numbers and the quotient is a signed zero (an ordinary u times it
+// is far under the scale's floor).  The exponent's argument stops at 200,
+// where exp is infinite or nothing beside 1 already, so that no product with
+// log2(e) leaves the range: t and r would be infinities of both signs for the
+// largest bf16 gates, and their result NaN.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  const float t = -g * kLog2e;
-  const float r = fmaf(-g, kLog2eLow, fmaf(-g, kLog2e, -t));
+  const float c = __builtin_amdgcn_fmed3f(g, -200.0f, 200.0f);
+  const float t = -c * kLog2e;
+  const float r = fmaf(-c, kLog2eLow, fmaf(-c, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t) * fmaf(r, kLn2, 1.0f);
   return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }

@@ -190,6 +190,30 @@ def test_silu_mul(M, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_silu_mul_largest_gates(dtype):
+    """Gates up to the type's largest: silu(g) u = g u above, 0 below -87.33.  Each
+    block holds one value y, so its scale is |y| / 448 within y's 8 half steps
+    and the division's one, and its numbers are +-448."""
+    top = torch.finfo(dtype).max
+    tiny = 1.0 / 1024 if dtype == torch.float16 else 2.0 ** -120
+    pairs = [(top, tiny), (top, -tiny), (0.75 * top, tiny), (0.6 * top, tiny), (300.0, 3.0), (-300.0, 3.0),
+             (-90.0, top), (-0.6 * top, 1.0), (-0.75 * top, 1.0), (-top, 1.0)]
+    GU = torch.tensor(pairs, dtype=torch.float64).to(dtype)[:, :, None].expand(-1, -1, 128).reshape(-1, 256).cuda()
+    q, s = i8.fp8_silu_mul(GU)
+    want = F.silu_mul64(f32(GU))[:, 0]
+    got, scale = F.e4m3_decode(raw(q)), s[0].cpu().numpy().astype(np.float64)
+    for i, y in enumerate(want):
+        if pairs[i][0] < -87.4:
+            assert not np.any(got[i]), pairs[i]
+        else:
+            assert np.all(got[i] == np.sign(y) * 448), pairs[i]
+            assert abs(scale[i] - abs(y) / 448) <= 9 * 2.0 ** -24 * abs(y) / 448, pairs[i]
+    bad = torch.tensor([[float("inf"), 1.0], [float("-inf"), 1.0], [float("nan"), 1.0], [1.0, float("inf")]])
+    q, s = i8.fp8_silu_mul(bad.to(dtype)[:, :, None].expand(-1, -1, 128).reshape(-1, 256).cuda())
+    assert np.all(raw(q) & 0x7f == 0x7f) and torch.isinf(s[0, 0]) and torch.isinf(s[0, 3])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("K,N", [(16, 16), (128, 128), (144, 272), (272, 144), (1040, 400)])
 def test_quantize_and_pack_weight(K, N, dtype):
     W = acts(K, N, dtype, N, std=0.02)
