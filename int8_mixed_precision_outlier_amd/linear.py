@@ -121,7 +121,7 @@ class Fp8BlockLinear(torch.nn.Module):
     x: fp16 or bf16 [..., in_features], or the pair (e4m3 [M, in_features],
     scales) that Fp8RMSNorm, fp8_quantize or fp8_silu_mul leaves; then y is
     [M, out_features].  y is of the module's 16-bit type, the weight's at
-    first.  Buffers: w_f8 (packed), w_scale, bias or None.  For serving: y
+    first; half() and bfloat16() change it, and never the weights.  Buffers: w_f8 (packed), w_scale, bias or None.  For serving: y
     carries no gradient.
     """
 
@@ -157,6 +157,21 @@ class Fp8BlockLinear(torch.nn.Module):
         torch.nn.Module.__init__(self)
         self._set(fp8_pack_weight(weight), w_scale.to(torch.float32).contiguous(), weight.shape[1],
                   dtype, bias)
+        return self
+
+    def _apply(self, fn, recurse=True):
+        # half(), to(torch.bfloat16) and the like choose the type of y and bias;
+        # the e4m3 numbers and their fp32 scales only follow to another device
+        held = {"w_f8": self.w_f8, "w_scale": self.w_scale}
+        probe = fn(torch.empty(0, dtype=self.dtype, device=self.w_f8.device))
+        super()._apply(fn, recurse)
+        for name, t in held.items():
+            if getattr(self, name).dtype != t.dtype:
+                setattr(self, name, t.to(getattr(self, name).device))
+        if probe.dtype in (torch.float16, torch.bfloat16):
+            self.dtype = probe.dtype
+        if self.bias is not None and self.bias.dtype != self.dtype:
+            self.bias = self.bias.to(self.dtype)
         return self
 
     def extra_repr(self) -> str:

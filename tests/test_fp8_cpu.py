@@ -164,6 +164,29 @@ def test_binding_wants_gpu_tensors():
         Fp8RMSNorm(x[0])
 
 
+def test_module_type_changes_leave_the_weights():
+    """half(), bfloat16(), float() and moves of a module around the layer: the
+    e4m3 bytes and fp32 scales stay, bias and y take the 16-bit types."""
+    from int8_mixed_precision_outlier_amd.linear import Fp8BlockLinear
+    layer = Fp8BlockLinear.__new__(Fp8BlockLinear)
+    torch.nn.Module.__init__(layer)
+    w = torch.arange(32 * 128).remainder(251).to(torch.uint8).view(32, 128).view(torch.float8_e4m3fn)
+    ws = torch.rand(1, 1)
+    layer._set(w.clone(), ws.clone(), 128, torch.bfloat16, torch.arange(32.0))
+    outer = torch.nn.Sequential(layer, torch.nn.Linear(32, 8))
+    for change, dtype in ((lambda: outer.half(), torch.float16), (lambda: outer.to(torch.bfloat16), torch.bfloat16),
+                          (lambda: outer.float(), torch.bfloat16), (lambda: outer.to("cpu"), torch.bfloat16),
+                          (lambda: layer.half(), torch.float16), (lambda: outer.double(), torch.float16)):
+        assert change() in (outer, layer)
+        assert layer.dtype == dtype and layer.bias.dtype == dtype
+        assert torch.equal(layer.bias.float(), torch.arange(32.0))
+        assert layer.w_f8.dtype == w.dtype and torch.equal(layer.w_f8.view(torch.uint8), w.view(torch.uint8))
+        assert layer.w_scale.dtype == torch.float32 and torch.equal(layer.w_scale, ws)
+        assert set(layer.state_dict()) == {"w_f8", "w_scale", "bias"}
+    meta = layer.to("meta")
+    assert meta.w_f8.device.type == "meta" and meta.to_empty(device="cpu").w_f8.dtype == w.dtype
+
+
 @needs_lib
 def test_kernel_choice_over_seeded_sizes():
     """The planner on 256 CUs over 4000 seeded sizes: streaming up to 64 tokens

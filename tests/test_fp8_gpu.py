@@ -501,6 +501,11 @@ def test_modules(dtype):
         layer(x[..., :16])
     with pytest.raises(ValueError):
         norm(x, x[:1])
+    other = TYPES[1 - TYPES.index(dtype)]
+    changed = Fp8BlockLinear.from_linear(lin).to(other)
+    want = i8.fp8_matmul(q, s, layer.w_f8, layer.w_scale, bias=lin.bias.detach().to(other))
+    assert torch.equal(changed((q, s)), want) and torch.equal(changed.to(dtype).w_f8.view(torch.uint8),
+                                                              layer.w_f8.view(torch.uint8))
     state = Fp8BlockLinear.from_linear(torch.nn.Linear(K, N, dtype=dtype, device="cuda"))
     state.load_state_dict(layer.state_dict())
     assert torch.equal(state(x), y)
