@@ -52,7 +52,8 @@ struct DecodeLds {
 template <int TY, int R, int T, int KS, int U>
 __global__ __launch_bounds__(KS * 64) void k_fp8_decode(
     const uint8_t* __restrict__ X, const float* __restrict__ xs, const uint8_t* __restrict__ W,
-    const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y, int M, int N, int K, int KB) {
+    const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y,
+    int M, int N, int K, int KB) {
   using L = DecodeLds<R, T, KS, U>;
   extern __shared__ __align__(16) int8_t smem[];
   const int lane = threadIdx.x & 63;

@@ -473,8 +473,9 @@ static hipError_t run_gemm(const Fp8Call& c, int nbase, int nend, hipStream_t st
   // groups of 4 token tiles: the 32 tiles an XCD runs at once share 4 token
   // and 8 feature panels in its L2 (4096x12288x49152: 1963 us; 2 tiles 2035,
   // 8 tiles 1975, 16 tiles 2040)
-  kern<<<tilesM * tilesN, (WM * WN + PW) * 64, shm, st>>>(c.X, c.xs, c.W, c.ws, c.bias, c.Y, c.M, c.N, c.K,
-                                                   KB, tilesM, tilesN, tilesM < 4 ? tilesM : 4, nbase);
+  kern<<<tilesM * tilesN, (WM * WN + PW) * 64, shm, st>>>(
+      c.X, c.xs, c.W, c.ws, c.bias, c.Y, c.M, c.N, c.K, KB, tilesM, tilesN,
+      tilesM < 4 ? tilesM : 4, nbase);
   return hipGetLastError();
 }
 
@@ -527,9 +528,9 @@ static int cheapest_tile(long M, long n, long cus, double* cost) {
     best = kTile256x128;
     *cost = c1;
   }
-  const double c2 = t128 <= cus ? kF128Deep
-                                : kF128 * (double)(t128 / (2 * cus)) +
-                                      (t128 % (2 * cus) == 0 ? 0.0 : t128 % (2 * cus) <= cus ? kF128Deep : kF128);
+  const long last = t128 % (2 * cus);
+  const double c2 = kF128 * (double)(t128 / (2 * cus)) +
+                    (last == 0 ? 0.0 : last <= cus ? kF128Deep : kF128);
   if (c2 < *cost) {
     best = t128 <= cus ? kTile128Deep : kTile128;
     *cost = c2;

@@ -48,9 +48,9 @@ def _tensor(t, name: str, dtypes, shape, device=None):
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     have = t.shape
-    if (len(have) != shape if isinstance(shape, int) else
-            have != shape and (len(have) != len(shape) or shape[0] is not None or have[1:] != shape[1:])):
-        want = ((None,) * shape if isinstance(shape, int) else shape)
+    if (len(have) != shape if isinstance(shape, int) else have != shape and (
+            len(have) != len(shape) or shape[0] is not None or have[1:] != shape[1:])):
+        want = (None,) * shape if isinstance(shape, int) else shape
         want = tuple("any" if w is None else w for w in want)
         raise ValueError(f"{name} must have shape {want}, got {tuple(have)}")
     if not t.is_contiguous():
