@@ -179,11 +179,15 @@ class Fp8BlockLinear(torch.nn.Module):
                 f"bias={self.bias is not None}, dtype={self.dtype}")
 
     def forward(self, x) -> torch.Tensor:
-        if not isinstance(x, torch.Tensor):
+        pair = not isinstance(x, torch.Tensor)
+        # for pairs too: the packed weight holds in_features only rounded up to
+        # 128, so the product takes another width as it comes
+        width = (x[0] if pair else x).shape[-1]
+        if width != self.in_features:
+            raise ValueError(f"expected last dimension {self.in_features}, got {width}")
+        if pair:
             q, s = x
             return fp8_matmul(q, s, self.w_f8, self.w_scale, bias=self.bias, out_dtype=self.dtype)
-        if x.shape[-1] != self.in_features:
-            raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
         q, s = fp8_quantize(x.reshape(-1, self.in_features).contiguous())
         y = fp8_matmul(q, s, self.w_f8, self.w_scale, bias=self.bias, out_dtype=self.dtype)
         return y.reshape(*x.shape[:-1], self.out_features)

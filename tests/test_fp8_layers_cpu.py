@@ -1,0 +1,32 @@
+"""The block-scaled e4m3 layers, what needs no GPU: refusals that come before
+any kernel, and changes of type."""
+import pytest
+import torch
+
+from int8_mixed_precision_outlier_amd.linear import Fp8BlockLinear
+
+E4M3 = torch.float8_e4m3fn
+
+
+def block_linear(K=272, N=32, dtype=torch.bfloat16, bias=None):
+    """A layer over buffers on the CPU, as a moved one: it refuses before it computes."""
+    layer = Fp8BlockLinear.__new__(Fp8BlockLinear)
+    torch.nn.Module.__init__(layer)
+    kb = -(-K // 128)
+    w = torch.arange(N * kb * 128).remainder(120).to(torch.uint8).view(N, kb * 128).view(E4M3)
+    layer._set(w, torch.rand(-(-N // 128), kb), K, dtype, bias)
+    return layer
+
+
+@pytest.mark.parametrize("K,wrong", [(272, (256, 288, 384, 400)), (384, (272, 368)), (16, (32, 128))])
+def test_pair_of_another_width(K, wrong):
+    """The packed weight keeps K rounded up to 128 only, so a pair of another
+    width would pass the product's own checks."""
+    layer = block_linear(K)
+    for k in wrong:
+        q = torch.zeros((5, k)).to(E4M3)
+        with pytest.raises(ValueError, match=f"{K}.*{k}"):
+            layer((q, torch.ones(-(-k // 128), 5)))
+    for k in (K + 16, 7):
+        with pytest.raises(ValueError, match=f"{K}.*{k}"):
+            layer(torch.zeros((5, k), dtype=torch.bfloat16))
