@@ -12,9 +12,11 @@ from __future__ import annotations
 
 import torch
 
-from . import (build_outlier_cache, fp8_matmul, fp8_pack_weight, fp8_quantize,
+from . import (FP8_BLOCK, build_outlier_cache, fp8_matmul, fp8_pack_weight, fp8_quantize,
                fp8_quantize_weight, fp8_rms_norm, mixed_matmul, mixed_matmul_cached,
                quantize_weight, workspace_size)
+
+_HALVES = (torch.float16, torch.bfloat16)
 
 
 class Int8MixedLinear(torch.nn.Module):
@@ -129,7 +131,7 @@ class Fp8BlockLinear(torch.nn.Module):
         super().__init__()
         if weight.dim() != 2 or weight.device.type != "cuda":
             raise TypeError("weight must be a 2-D CUDA tensor [out_features, in_features]")
-        if weight.dtype not in (torch.float16, torch.bfloat16):
+        if weight.dtype not in _HALVES:
             raise TypeError(f"weight must be fp16 or bf16, got {weight.dtype}")
         w_f8, w_scale = fp8_quantize_weight(weight.detach().t().contiguous())
         self._set(w_f8, w_scale, weight.shape[1], weight.dtype, bias)
@@ -138,6 +140,8 @@ class Fp8BlockLinear(torch.nn.Module):
         self.register_buffer("w_f8", w_f8)
         self.register_buffer("w_scale", w_scale)
         if bias is not None:
+            if bias.shape != w_f8.shape[:1]:
+                raise ValueError(f"bias must have shape {tuple(w_f8.shape[:1])}, got {tuple(bias.shape)}")
             bias = bias.detach().to(device=w_f8.device, dtype=dtype).contiguous()
         self.register_buffer("bias", bias)
         self.in_features, self.out_features = in_features, w_f8.shape[0]
@@ -152,11 +156,18 @@ class Fp8BlockLinear(torch.nn.Module):
                        bias: torch.Tensor | None = None,
                        dtype: torch.dtype = torch.bfloat16) -> "Fp8BlockLinear":
         """A checkpoint's e4m3 weight [out, in] with its scales
-        [ceil(out/128), ceil(in/128)]."""
+        [ceil(out/128), ceil(in/128)]; y is of `dtype`, fp16 or bf16."""
+        if weight.dim() != 2:
+            raise TypeError("weight must be a 2-D CUDA tensor [out_features, in_features]")
+        if dtype not in _HALVES:
+            raise TypeError(f"dtype must be fp16 or bf16, got {dtype}")
+        blocks = tuple((n + FP8_BLOCK - 1) // FP8_BLOCK for n in weight.shape)
+        if w_scale.shape != blocks:
+            raise ValueError(f"w_scale must have shape {blocks}, got {tuple(w_scale.shape)}")
         self = cls.__new__(cls)
         torch.nn.Module.__init__(self)
-        self._set(fp8_pack_weight(weight), w_scale.to(torch.float32).contiguous(), weight.shape[1],
-                  dtype, bias)
+        w_scale = w_scale.detach().to(device=weight.device, dtype=torch.float32).contiguous()
+        self._set(fp8_pack_weight(weight.detach()), w_scale, weight.shape[1], dtype, bias)
         return self
 
     def _apply(self, fn, recurse=True):
@@ -168,7 +179,7 @@ class Fp8BlockLinear(torch.nn.Module):
         for name, t in held.items():
             if getattr(self, name).dtype != t.dtype:
                 setattr(self, name, t.to(getattr(self, name).device))
-        if probe.dtype in (torch.float16, torch.bfloat16):
+        if probe.dtype in _HALVES:
             self.dtype = probe.dtype
         if self.bias is not None and self.bias.dtype != self.dtype:
             self.bias = self.bias.to(self.dtype)

@@ -30,3 +30,26 @@ def test_pair_of_another_width(K, wrong):
     for k in (K + 16, 7):
         with pytest.raises(ValueError, match=f"{K}.*{k}"):
             layer(torch.zeros((5, k), dtype=torch.bfloat16))
+
+
+def test_from_quantized_looks_at_its_arguments():
+    """Scales, bias and types that no forward could take are refused when the
+    layer is built."""
+    w = torch.zeros((144, 272)).to(E4M3)  # scales [2, 3]
+    make = lambda scale=(2, 3), **k: Fp8BlockLinear.from_quantized(w, torch.ones(scale), **k)  # noqa: E731
+    for scale in ((3, 2), (2, 2), (1, 3), (6,), (2, 3, 1), ()):
+        with pytest.raises(ValueError, match=r"w_scale.*\(2, 3\)"):
+            make(scale)
+    for dtype in (torch.float32, E4M3, torch.int8):
+        with pytest.raises(TypeError, match="dtype"):
+            make(dtype=dtype)
+    with pytest.raises(TypeError, match="2-D"):
+        Fp8BlockLinear.from_quantized(w[0], torch.ones(2, 3))
+    with pytest.raises(TypeError, match="CUDA"):
+        make()  # the weight itself: packing is the GPU's
+
+
+@pytest.mark.parametrize("shape", [(31,), (272,), (32, 1), ()])
+def test_bias_of_another_size(shape):
+    with pytest.raises(ValueError, match="bias"):
+        block_linear(bias=torch.zeros(shape))

@@ -23,3 +23,14 @@ def test_pair_of_another_width():
             layer(i8.fp8_quantize(acts(5, k, torch.bfloat16, 2)))
     x = acts(5, 272, torch.bfloat16, 3)
     assert torch.equal(layer(i8.fp8_quantize(x)), layer(x))
+
+
+def test_from_quantized_scales_from_elsewhere():
+    """A checkpoint's scales as a parameter on the host: moved, and no parameter
+    of the layer."""
+    w = acts(32, 272, torch.float32, 4).to(E4M3)
+    ws = torch.rand(1, 3)
+    layer = Fp8BlockLinear.from_quantized(w, torch.nn.Parameter(ws))
+    x = acts(5, 272, torch.bfloat16, 5)
+    assert torch.equal(layer(x), i8.fp8_matmul(*i8.fp8_quantize(x), i8.fp8_pack_weight(w), ws.cuda()))
+    assert not list(layer.parameters()) and not layer.w_scale.requires_grad
