@@ -364,6 +364,8 @@ int int8mm_kernel_config(int64_t M, int64_t N, int64_t K, int32_t *cfg);
  *     call have one type.
  *   - KB = ceil(K / 128).  K may end inside a block: its scale is that of
  *     the columns there are.
+ *   - A weight has N * 128 <= INT8MM_MAX_MN, for K == 0 too (for K > 0 that
+ *     follows from N * roundup(K, 128) <= INT8MM_MAX_MN).
  *   - Quantization of a block with absmax a = max(max |x|, 2^-100):
  *     scale = RN32(a / 448), q = e4m3_rne(RN32(x * RN32(448 / a))), x ~ q * scale.
  *     fp8_quantize is therefore reproducible bit for bit.

@@ -22,8 +22,10 @@ int check_rows(int type, int64_t rows, int64_t K, int64_t width) {
   return K % 16 != 0 ? INT8MM_EALIGN : INT8MM_OK;
 }
 
+// N * 128 <= INT8MM_MAX_MN follows from the product's bound where K > 0; it
+// keeps N within the kernels' integers and grids where K == 0.
 int check_weight(int64_t K, int64_t N) {
-  if (K < 0 || K > INT8MM_MAX_K || N < 0 || N > INT8MM_MAX_MN) return INT8MM_EINVAL;
+  if (K < 0 || K > INT8MM_MAX_K || N < 0 || N > INT8MM_MAX_MN / kFp8Block) return INT8MM_EINVAL;
   if (N * fp8_kpad(K) > INT8MM_MAX_MN) return INT8MM_EINVAL;
   return K % 16 != 0 || N % 16 != 0 ? INT8MM_EALIGN : INT8MM_OK;
 }
