@@ -91,8 +91,8 @@ class Fp8RMSNorm(torch.nn.Module):
     """The root-mean-square norm in front of Fp8BlockLinear layers, with the
     residual's addition: forward(x, residual) gives ((e4m3, scales), h) with
     h = x + residual, forward(x) the pair (e4m3, scales) alone.  x [..., K] of
-    the weight's type; the pair is 2-D, one row per token, and every
-    Fp8BlockLinear that reads this norm takes it as it is.
+    the weight's type, which half() and bfloat16() change; the pair is 2-D, one
+    row per token, and every Fp8BlockLinear that reads this norm takes it as it is.
     """
 
     def __init__(self, weight: torch.Tensor, eps: float = 1e-6):
@@ -101,6 +101,15 @@ class Fp8RMSNorm(torch.nn.Module):
             raise TypeError("weight must be a 1-D CUDA tensor")
         self.register_buffer("weight", weight.detach().clone())
         self.eps = float(eps)
+
+    def _apply(self, fn, recurse=True):
+        # half() and bfloat16() change the weight's type; float() and the like,
+        # to a type that the operator does not take, only move it
+        held = self.weight
+        super()._apply(fn, recurse)
+        if self.weight.dtype != held.dtype and self.weight.dtype not in _HALVES:
+            self.weight = held.to(self.weight.device)
+        return self
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
         K = self.weight.numel()

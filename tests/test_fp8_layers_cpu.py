@@ -3,7 +3,7 @@ any kernel, and changes of type."""
 import pytest
 import torch
 
-from int8_mixed_precision_outlier_amd.linear import Fp8BlockLinear
+from int8_mixed_precision_outlier_amd.linear import Fp8BlockLinear, Fp8RMSNorm
 
 E4M3 = torch.float8_e4m3fn
 
@@ -53,3 +53,21 @@ def test_from_quantized_looks_at_its_arguments():
 def test_bias_of_another_size(shape):
     with pytest.raises(ValueError, match="bias"):
         block_linear(bias=torch.zeros(shape))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_norm_keeps_a_16_bit_type(dtype):
+    """float(), double() and to(e4m3) of a model leave the norm a weight that it
+    takes, as they leave the linear layers; half() and bfloat16() change it."""
+    norm = Fp8RMSNorm.__new__(Fp8RMSNorm)
+    torch.nn.Module.__init__(norm)
+    w = (torch.arange(64) / 7).to(dtype)
+    norm.register_buffer("weight", w.clone())
+    outer = torch.nn.Sequential(norm, torch.nn.Linear(4, 4))
+    for change in (outer.float, outer.double, lambda: outer.to(E4M3), lambda: outer.to("cpu"), norm.float):
+        change()
+        assert norm.weight.dtype == dtype and torch.equal(norm.weight, w)
+        assert set(norm.state_dict()) == {"weight"}
+    assert outer.half()[0].weight.dtype == torch.float16
+    assert outer.to(torch.bfloat16)[0].weight.dtype == torch.bfloat16
+    assert norm.to("meta").to_empty(device="cpu").weight.dtype == torch.bfloat16

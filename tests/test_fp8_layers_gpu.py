@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import int8_mixed_precision_outlier_amd as i8
-from int8_mixed_precision_outlier_amd.linear import Fp8BlockLinear
+from int8_mixed_precision_outlier_amd.linear import Fp8BlockLinear, Fp8RMSNorm
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,18 @@ def test_from_quantized_scales_from_elsewhere():
     x = acts(5, 272, torch.bfloat16, 5)
     assert torch.equal(layer(x), i8.fp8_matmul(*i8.fp8_quantize(x), i8.fp8_pack_weight(w), ws.cuda()))
     assert not list(layer.parameters()) and not layer.w_scale.requires_grad
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+def test_model_after_float(dtype):
+    """A norm and the layer behind it give after float() what they gave before."""
+    K = 272
+    model = torch.nn.ModuleList([Fp8RMSNorm(acts(1, K, dtype, 6)[0]), Fp8BlockLinear(acts(32, K, dtype, 7))])
+    x, r = acts(5, K, dtype, 8), acts(5, K, dtype, 9)
+
+    def run():
+        pair, h = model[0](x, r)
+        return model[1](pair), h
+    want = run()
+    model.float()
+    assert all(torch.equal(a, b) and a.dtype == dtype for a, b in zip(run(), want))
