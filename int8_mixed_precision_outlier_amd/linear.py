@@ -182,7 +182,7 @@ class Fp8BlockLinear(torch.nn.Module):
     def _apply(self, fn, recurse=True):
         # half(), to(torch.bfloat16) and the like choose the type of y and bias;
         # the e4m3 numbers and their fp32 scales only follow to another device
-        held = {"w_f8": self.w_f8, "w_scale": self.w_scale}
+        held, bias = {"w_f8": self.w_f8, "w_scale": self.w_scale}, self.bias
         probe = fn(torch.empty(0, dtype=self.dtype, device=self.w_f8.device))
         super()._apply(fn, recurse)
         for name, t in held.items():
@@ -190,8 +190,8 @@ class Fp8BlockLinear(torch.nn.Module):
                 setattr(self, name, t.to(getattr(self, name).device))
         if probe.dtype in _HALVES:
             self.dtype = probe.dtype
-        if self.bias is not None and self.bias.dtype != self.dtype:
-            self.bias = self.bias.to(self.dtype)
+        if bias is not None and self.bias.dtype != self.dtype:  # from the bias as it was
+            self.bias = bias.to(device=self.bias.device, dtype=self.dtype)
         return self
 
     def extra_repr(self) -> str:

@@ -71,3 +71,15 @@ def test_norm_keeps_a_16_bit_type(dtype):
     assert outer.half()[0].weight.dtype == torch.float16
     assert outer.to(torch.bfloat16)[0].weight.dtype == torch.bfloat16
     assert norm.to("meta").to_empty(device="cpu").weight.dtype == torch.bfloat16
+
+
+def test_bias_survives_types_of_fewer_bits():
+    """to(e4m3) of a model around the layer leaves its bias unrounded."""
+    b = torch.linspace(-1, 1, 32).to(torch.bfloat16)
+    layer = block_linear(bias=b)
+    torch.nn.Sequential(layer).to(E4M3)
+    assert layer.dtype == layer.bias.dtype == torch.bfloat16 and torch.equal(layer.bias, b)
+    w, ws = layer.w_f8.view(torch.uint8).clone(), layer.w_scale.clone()
+    layer.to(torch.float8_e5m2).float()
+    assert torch.equal(layer.bias, b) and torch.equal(layer.w_scale, ws)
+    assert layer.w_f8.dtype == E4M3 and torch.equal(layer.w_f8.view(torch.uint8), w)
