@@ -435,7 +435,7 @@ int fp8_rms_norm(const void *X, const void *residual, const void *weight,
  * fp8_silu_mul -- the gated activation before a feed-forward's second
  * product: gate_up [M][2K] (16-bit; a row is its K gates, then its K ups) ->
  * the quantized g / (1 + exp(-g)) * u, in fp32 up to the quantizer.  Finite
- * gates below -87.33, where 1 / (1 + exp(-g)) is no normal fp32 number, give 0.
+ * gates below -88.72, whose exp(-g) passes fp32's range, give 0.
  * M * 2K <= INT8MM_MAX_MN.
  */
 int fp8_silu_mul(const void *gate_up, int type, int64_t M, int64_t K,

@@ -38,23 +38,29 @@ __device__ __forceinline__ uint2 quant8(const float (&y)[8], float& scale) {
 
 // silu(g) * u = g / (1 + exp(-g)) * u in fp32.  exp(-g) is 2^t times a
 // correction for what t = -g log2(e) loses in its rounding (and log2(e) in
-// its own), so that its error stays at the exponential instruction's, and
-// the quotient is a product with the reciprocal instruction's result: within
-// 8 half steps in all, at a third of the instructions of expf and the IEEE
-// division, which bound this kernel (2048x20480 with two blocks per group:
-// 37.9 us; with expf and four: 50.8).  Below g = -87.33 the reciprocal leaves
-// the normal numbers and the quotient is a signed zero (an ordinary u times it
-// is far under the scale's floor).  The exponent's argument stops at 200,
-// where exp is infinite or nothing beside 1 already, so that no product with
-// log2(e) leaves the range: t and r would be infinities of both signs for the
-// largest bf16 gates, and their result NaN.
+// its own), and the quotient is a product with the reciprocal instruction's
+// result, at a third of the instructions of expf and the IEEE division, which
+// bound this kernel (2048x20480 with two blocks per group: 37.9 us; with expf
+// and four: 50.8).  Within 8 half steps of 2^-24: the exponential and the
+// reciprocal instruction 2 each, the correction (second-order terms and the
+// rest of log2(e) add 2^-34), its fma to 1 + exp(-g) and the last two products
+// 1 each.  The reciprocal is taken of (1 + exp(-g)) / 256 and the gate divided
+// by 256, both exact: below g = -87.33 that of 1 + exp(-g) would leave the
+// normal numbers, where the instruction gives 0, and so would y though a bf16
+// u can be 3e38 (the gate's scaling costs 3 %, 2048x20480 bf16 36.8 -> 38.2 us).
+// From g = -88.73 on exp(-g) is infinite and y a signed zero.
+// The exponent's argument stops at 200, where exp is infinite or nothing
+// beside 1 already, so that no product with log2(e) leaves the range: t and r
+// would be infinities of both signs for the largest bf16 gates, and their
+// result NaN.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  constexpr float kScale = 0x1p-8f;
   const float c = __builtin_amdgcn_fmed3f(g, -200.0f, 200.0f);
   const float t = -c * kLog2e;
   const float r = fmaf(-c, kLog2eLow, fmaf(-c, kLog2e, -t));
-  const float e = __builtin_amdgcn_exp2f(t) * fmaf(r, kLn2, 1.0f);
-  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+  const float d = fmaf(__builtin_amdgcn_exp2f(t), fmaf(r, kLn2 * kScale, kScale), kScale);
+  return g * kScale * __builtin_amdgcn_rcpf(d) * u;
 }
 
 }  // namespace

@@ -1,0 +1,59 @@
+"""Block-scaled e4m3 operators on the GPU at the edges of their ranges, against
+the 64-bit oracle (oracle/fp8_block.py)."""
+import numpy as np
+import pytest
+import torch
+
+import int8_mixed_precision_outlier_amd as i8
+from oracle import fp8_block as F
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float16, torch.bfloat16]
+E4M3 = torch.float8_e4m3fn
+
+
+def f32(t):
+    return t.detach().float().cpu().numpy()
+
+
+def raw(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy()
+
+
+# Half steps (2^-24) of the gated product: the exponential instruction 2, its
+# correction 1, the fma that joins them to 1 + exp(-g) 1, the reciprocal
+# instruction 2, the products with gate and up 1 each; a hundredth for the
+# second-order terms.  The argument's remainder and log2(e)'s are in the
+# correction, the scalings by powers of two are exact.  The division by 448 adds
+# one to the scale's.
+GATE = 8.01 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_silu_mul_far_gates(dtype):
+    """Gates whose 1 / (1 + exp(-g)) is no normal fp32 number, and subnormal
+    gates, beside ups of the type's largest.  Each block holds one value."""
+    top, least = torch.finfo(dtype).max, torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    gates = [-86.0, -87.0, -87.25, -87.5, -88.0, -88.25, -88.5, least, -least, 5 * least]
+    if dtype == torch.float16:
+        gates += [-87.3125, -87.375, -88.6875]
+    ups = [top, -top, top / 16, 1e30 if dtype == torch.bfloat16 else 1e3]
+    GU = torch.tensor([(g, u) for g in gates for u in ups], dtype=torch.float64).to(dtype)
+    q, s = i8.fp8_silu_mul(GU[:, :, None].expand(-1, -1, 128).reshape(-1, 256).cuda())
+    y = F.silu_mul64(f32(GU))[:, 0]
+    s, v = s[0].cpu().numpy().astype(np.float64), F.e4m3_decode(raw(q))
+    s64 = np.maximum(np.abs(y), 2.0 ** -100) / 448
+    assert np.all(np.abs(s - s64) <= (GATE + 2.0 ** -24) * s64), (GU, s / s64 - 1)
+    want = (y / s)[:, None]
+    tol = np.maximum(np.abs(want) * 2.0 ** -4, 2.0 ** -10) + (2 * GATE + 2.0 ** -22) * np.abs(want)
+    assert np.all(np.abs(v - want) <= tol), GU[np.any(np.abs(v - want) > tol, 1)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_silu_mul_gates_past_exp(dtype):
+    """exp(-g) past fp32's range: a zero, whatever the finite up."""
+    top = torch.finfo(dtype).max
+    GU = torch.tensor([(g, u) for g in (-89.0, -100.0, -top) for u in (top, -top, 1.0)], dtype=torch.float64)
+    q, _ = i8.fp8_silu_mul(GU.to(dtype)[:, :, None].expand(-1, -1, 128).reshape(-1, 256).cuda())
+    assert not np.any(F.e4m3_decode(raw(q)))
