@@ -11,7 +11,8 @@ Activations and weights are fp16 or bf16; e4m3 tensors are
 torch.float8_e4m3fn.  Serving operators: their results carry no gradient.
 Each call runs on the device of its first tensor, on that device's current
 stream unless `stream` is given; buffers a call allocates are allocated on
-its stream.
+its stream, and tensors given to a call with a `stream` may be dropped as soon
+as it returns, as with any other call.
 """
 from __future__ import annotations
 
@@ -73,11 +74,18 @@ def _elsewhere(t, stream) -> bool:
 
 
 @contextlib.contextmanager
-def _current(t, stream):
+def _current(t, stream, *others):
+    """t's device and `stream` made current for a call on t and `others`."""
     if stream is not None and stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
     with torch.cuda.device(t.device), torch.cuda.stream(stream):
         yield
+    if stream is not None:
+        # the allocator gives a tensor's memory away in the order of the stream
+        # it was allocated on: not before this one is through with it either
+        for u in (t, *others):
+            if u is not None:
+                u.record_stream(stream)
 
 
 def _at(t):
@@ -131,7 +139,7 @@ def fp8_quantize(X: torch.Tensor, out=None, stream=None):
     `out`: such a pair to write into."""
     _tensor(X, "X", _HALVES, 2)
     if _elsewhere(X, stream):
-        with _current(X, stream):
+        with _current(X, stream, *(out or ())):
             return fp8_quantize(X, out=out)
     M, K = X.shape
     X_f8, x_scale = _quantized(out, M, K, X.device, X)
@@ -149,7 +157,7 @@ def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     `residual_out` takes H; it may be `residual` itself."""
     _tensor(X, "X", _HALVES, 2)
     if _elsewhere(X, stream):
-        with _current(X, stream):
+        with _current(X, stream, weight, residual, residual_out, *(out or ())):
             return fp8_rms_norm(X, weight, eps, residual, residual_out, out)
     M, K = X.shape
     _tensor(weight, "weight", (X.dtype,), (K,), X.device)
@@ -174,7 +182,7 @@ def fp8_silu_mul(gate_up: torch.Tensor, out=None, stream=None):
     silu(gate) * up: (A_f8 e4m3 [M,K], a_scale fp32 [ceil(K/128), M])."""
     _tensor(gate_up, "gate_up", _HALVES, 2)
     if _elsewhere(gate_up, stream):
-        with _current(gate_up, stream):
+        with _current(gate_up, stream, *(out or ())):
             return fp8_silu_mul(gate_up, out=out)
     M, K2 = gate_up.shape
     if K2 % 2:
@@ -196,7 +204,7 @@ def fp8_matmul(X_f8: torch.Tensor, x_scale: torch.Tensor, W_f8: torch.Tensor,
     `out_dtype` (fp16 or bf16; by default that of `out`, else of bias, else bf16)."""
     _tensor(X_f8, "X_f8", (_E4M3,), 2)
     if _elsewhere(X_f8, stream):
-        with _current(X_f8, stream):
+        with _current(X_f8, stream, x_scale, W_f8, w_scale, bias, out):
             return fp8_matmul(X_f8, x_scale, W_f8, w_scale, bias, out_dtype, out)
     M, K = X_f8.shape
     dev = X_f8.device

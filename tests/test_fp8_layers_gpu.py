@@ -49,3 +49,38 @@ def test_model_after_float(dtype):
     want = run()
     model.float()
     assert all(torch.equal(a, b) and a.dtype == dtype for a, b in zip(run(), want))
+
+
+def test_tensors_given_to_another_stream_may_be_dropped():
+    """A call with `stream` reads tensors of the current stream.  While that
+    stream is busy, new tensors of the current one get other memory than the
+    operands that the caller no longer holds."""
+    M = K = N = 4096
+    half = torch.bfloat16
+    stream = torch.cuda.Stream()
+    w = torch.zeros((4 * N, 4 * K), device="cuda", dtype=half)
+    busy = [*i8.fp8_quantize(torch.zeros((M, 4 * K), device="cuda", dtype=half)), *i8.fp8_quantize_weight(w)]
+    del w
+    x, gu, g = acts(M, K, half, 1), acts(M, 2 * K, half, 2), acts(1, K, half, 3)[0]
+    q, s = i8.fp8_quantize(x)
+    calls = [(i8.fp8_quantize, lambda: (x.clone(),)), (i8.fp8_silu_mul, lambda: (gu.clone(),)),
+             (i8.fp8_rms_norm, lambda: (x.clone(), g.clone(), 1e-6, x.clone())),
+             (i8.fp8_quantize_weight, lambda: (x.clone(),)), (i8.fp8_pack_weight, lambda: (q.clone(),)),
+             (i8.fp8_matmul, lambda: (q.clone(), s.clone(), *i8.fp8_quantize_weight(x)))]
+    for call, operands in calls:
+        want = call(*operands())
+        args = operands()
+        torch.cuda.synchronize()
+        for _ in range(24):  # about 20 ms
+            i8.fp8_matmul(*busy, stream=stream)
+        got = call(*args, stream=stream)
+        held = [(a.data_ptr(), a.shape, a.dtype) for a in args if isinstance(a, torch.Tensor)]
+        del args
+        new = [torch.empty(shape, dtype=dtype, device="cuda") for _, shape, dtype in held for _ in range(2)]
+        assert not stream.query(), "the stream was to be busy meanwhile"
+        assert not {t.data_ptr() for t in new} & {p for p, _, _ in held}, call
+        for t in new:
+            t.view(torch.uint8).fill_(0x7f)
+        torch.cuda.synchronize()
+        pairs = zip(got, want) if isinstance(got, tuple) else [(got, want)]
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in pairs), call
