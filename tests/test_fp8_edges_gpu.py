@@ -57,3 +57,37 @@ def test_silu_mul_gates_past_exp(dtype):
     GU = torch.tensor([(g, u) for g in (-89.0, -100.0, -top) for u in (top, -top, 1.0)], dtype=torch.float64)
     q, _ = i8.fp8_silu_mul(GU.to(dtype)[:, :, None].expand(-1, -1, 128).reshape(-1, 256).cuda())
     assert not np.any(F.e4m3_decode(raw(q)))
+
+
+def integers(rows, cols, seed):
+    """e4m3 codes of the integers -4 .. 4 on the GPU."""
+    table = torch.from_numpy(F.e4m3_encode(np.arange(-4, 5))).cuda()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    out = torch.empty((rows, cols), dtype=torch.uint8, device="cuda")
+    step = max(1, (1 << 28) // cols)
+    for r in range(0, rows, step):
+        n = min(step, rows - r)
+        out[r:r + n] = table[torch.randint(0, 9, (n, cols), generator=g, device="cuda", dtype=torch.int32)]
+    return out
+
+
+@pytest.mark.parametrize("K", [65536, 65520])
+@pytest.mark.parametrize("M,N", [(1, 32768), (40, 32768), (32768, 16), (130, 32768)])
+def test_matmul_ends_of_the_largest_operands(M, N, K):
+    """Operands of up to 2^31 bytes.  The tokens are zero but for the first and
+    the last K block, the scales are one, so the product is a sum of 256
+    integers at most, exact up to the result's rounding: a last block that is
+    not read, or read from elsewhere, shows."""
+    x, w = integers(M, K, 1), integers(N, K, 2)
+    last = (K - 1) // 128 * 128
+    x[:, 128:last] = 0
+    ones = lambda *s: torch.ones(s, device="cuda")  # noqa: E731
+    Y = i8.fp8_matmul(x.view(E4M3), ones(-(-K // 128), M), i8.fp8_pack_weight(w.view(E4M3)),
+                      ones(-(-N // 128), -(-K // 128)), out_dtype=torch.float16)
+    m = sorted({0, M // 2, max(0, M - 3), max(0, M - 2), M - 1})
+    n = [*range(16), *range(N - 16, N)] if N > 32 else list(range(N))
+    want = F.e4m3_decode(raw(x[m])) @ F.e4m3_decode(raw(w[n])).T
+    assert np.array_equal(Y[m][:, n].cpu().numpy(), want.astype(np.float16))
+    assert len(np.unique(want)) > 2
+    if M > 1:  # every row has a last block of its own
+        assert not torch.equal(Y[-1], Y[-2])
