@@ -91,3 +91,33 @@ def test_matmul_ends_of_the_largest_operands(M, N, K):
     assert len(np.unique(want)) > 2
     if M > 1:  # every row has a last block of its own
         assert not torch.equal(Y[-1], Y[-2])
+
+
+def test_two_streams_overlap():
+    """Calls in turn on two streams, enqueued faster than they run, give what
+    they give alone."""
+    def operands(M, K, N, seed):
+        x, w = integers(M, K, seed).view(E4M3), i8.fp8_pack_weight(integers(N, K, seed + 1).view(E4M3))
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.rand(s, generator=g, device="cuda")  # noqa: E731
+        return x, rnd(K // 128, M), w, rnd(-(-N // 128), K // 128)
+    args = [operands(40, 12288, 12288, 1), operands(300, 8192, 8192, 3)]
+    gate = [torch.randn((512, 16384), device="cuda").to(torch.bfloat16) for _ in args]
+    call = lambda k: (i8.fp8_matmul(*args[k]), *i8.fp8_silu_mul(gate[k]))  # noqa: E731
+    alone = [call(k) for k in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    ends = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in args]
+    got = []
+    for r in range(30):
+        for k, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                if r == 0:
+                    ends[k][0].record()
+                got.append((k, call(k)))
+                if r == 29:
+                    ends[k][1].record()
+    torch.cuda.synchronize()
+    assert ends[0][0].elapsed_time(ends[1][1]) > 0 and ends[1][0].elapsed_time(ends[0][1]) > 0
+    for k, outs in got:
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs, alone[k]))
