@@ -1,5 +1,9 @@
 """Block-scaled e4m3 operators on the GPU at the edges of their ranges, against
 the 64-bit oracle (oracle/fp8_block.py)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -121,3 +125,46 @@ def test_two_streams_overlap():
     assert ends[0][0].elapsed_time(ends[1][1]) > 0 and ends[1][0].elapsed_time(ends[0][1]) > 0
     for k, outs in got:
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs, alone[k]))
+
+
+CAPTURE = """
+import sys
+import torch
+sys.path.insert(0, {root!r})
+import int8_mixed_precision_outlier_amd as i8
+M, N, K = {sizes}
+assert i8.fp8_matmul_config(M, N, K)[0] == {kind!r}
+g = torch.Generator(device="cuda").manual_seed(1)
+code = lambda *s: torch.randint(0, 120, s, generator=g, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+w = i8.fp8_pack_weight(code(N, K))
+ws = torch.rand((-(-N // 128), -(-K // 128)), device="cuda") * 1e-3
+x, res = (torch.randn((M, K), generator=g, device="cuda").bfloat16() for _ in range(2))
+weight = x[0].clone()
+def chain():
+    q, s, h = i8.fp8_rms_norm(x, weight, residual=res)
+    y = i8.fp8_matmul(q, s, w, ws)
+    return (q, s, h, y, *i8.fp8_silu_mul(y), *i8.fp8_quantize(h))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = chain()
+for k in range(3):
+    x.copy_(torch.randn((M, K), generator=g, device="cuda"))
+    graph.replay()
+    torch.cuda.synchronize()
+    want = chain()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(out, want)), k
+print("replays equal")
+"""
+
+
+@pytest.mark.parametrize("sizes,kind", [((5, 4096, 528), "decode"), ((200, 2080, 528), "tiled"),
+                                        ((1900, 9600, 272), "split")])
+def test_first_calls_of_a_process_inside_a_capture(sizes, kind):
+    """A process whose first norm, product, gate and quantizer are captured: no
+    module is loaded and no limit raised before the capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE.format(root=root, sizes=sizes, kind=kind)],
+                       capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and r.stdout.strip() == "replays equal", r.stderr[-2000:]
