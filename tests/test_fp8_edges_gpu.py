@@ -168,3 +168,37 @@ def test_first_calls_of_a_process_inside_a_capture(sizes, kind):
     r = subprocess.run([sys.executable, "-c", CAPTURE.format(root=root, sizes=sizes, kind=kind)],
                        capture_output=True, text=True, timeout=100)
     assert r.returncode == 0 and r.stdout.strip() == "replays equal", r.stderr[-2000:]
+
+
+def unpacked(w, N, KB):
+    """The packed weight's rows, for blocks of 16 rows at a time: [N, KB * 128]."""
+    return w.view(torch.uint8).view(-1, KB, 8, 16, 16).permute(0, 3, 1, 2, 4).reshape(N, KB * 128)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("K,N", [(4096, 12288), (5136, 20464), (65536, 32768), (65520, 32752), (16, 1 << 24)])
+def test_quantize_weight_large(K, N, dtype):
+    """Every scale and number of large weights, bit for bit, 128 features at a
+    time for some of them and the last: the quotients are those of 64 bits
+    rounded to 32, which is what a 32-bit division gives."""
+    KB = -(-K // 128)
+    g = torch.Generator(device="cuda").manual_seed(K + N)
+    W = torch.empty((K, N), dtype=dtype, device="cuda")
+    for k in range(0, K, 4096):
+        rows = min(4096, K - k)
+        for n in range(0, N, 1 << 20):
+            cols = min(1 << 20, N - n)
+            W[k:k + rows, n:n + cols] = torch.randn((rows, cols), generator=g, device="cuda") * 0.02
+    w, ws = i8.fp8_quantize_weight(W)
+    assert w.shape == (N, KB * 128) and ws.shape == (-(-N // 128), KB)
+    nbs = sorted({*range(0, ws.shape[0], max(1, ws.shape[0] // 12)), ws.shape[0] - 1})
+    for nb in nbs:
+        cols = slice(nb * 128, min(N, nb * 128 + 128))
+        n = cols.stop - cols.start
+        t = torch.zeros((n, KB * 128), device="cuda")
+        t[:, :K] = W[:, cols].t().float()
+        t = t.view(n, KB, 128)
+        a = t.abs().amax((0, 2)).clamp(min=2.0 ** -100).double()
+        assert torch.equal(ws[nb], (a / 448).float()), nb
+        q = (t * (448 / a).float()[None, :, None]).view(n, KB * 128).to(E4M3)
+        assert torch.equal(unpacked(w[cols], n, KB), q.view(torch.uint8)), nb
