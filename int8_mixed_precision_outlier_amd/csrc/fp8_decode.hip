@@ -3,8 +3,8 @@
 // whose 16 columns are tokens.
 //
 // A workgroup owns R blocks of 16 features over all of K, so nothing is
-// combined across workgroups; its KS wavefronts take the K blocks in turn, U
-// at a time, and add their partial sums through LDS at the end in a fixed
+// combined across workgroups; its KS wavefronts take the K blocks in turn and
+// add their partial sums through LDS at the end in a fixed
 // order.  A wavefront's K block of 16 features is 2 KB of contiguous W, two
 // 16-byte loads per lane in exactly the MFMA's operand layout (nontemporal:
 // the stream is never read again).  The tokens' bytes and scales reach a part
@@ -12,8 +12,8 @@
 // instruction moves 8 rows x 128 bytes, whole cache lines, with the chunks of
 // a row swapped as in fp8_gemm.hip, where 16 rows x 64 bytes straight into
 // registers fetched each line twice (a CU then took in 38 GB/s, too little
-// for HBM's rate at more than 16 tokens: 32x20480x5120 33.6 us).  The next U K
-// blocks are on their way under the MFMAs and scaling fmas of the current ones.
+// for HBM's rate at more than 16 tokens: 32x20480x5120 33.6 us).  The next K
+// block is on its way under the MFMAs and scaling fmas of the current one.
 //
 // Bound by HBM for a few tokens (1x12288x49152: 86 us = 7.0 TB/s, 32x12288x36864:
 // 71 us = 6.4 TB/s), by what a CU takes in of both operands (about 55 GB/s)
@@ -37,24 +37,24 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("" ::: "memory");
 }
 
-// LDS: two stages of U K blocks per wavefront, each T x 16 rows of 128 bytes
+// LDS: two stages of a K block per wavefront, each T x 16 rows of 128 bytes
 // and their scales (64 tokens per DMA); at the end the partial sums.
-template <int R, int T, int KS, int U>
+template <int R, int T, int KS>
 struct DecodeLds {
   static constexpr int SDMA = (T + 3) / 4;  // DMAs of 64 token scales
   static constexpr int BLOCK = T * 2048 + SDMA * 256;
-  static constexpr int WAVE = 2 * U * BLOCK;
+  static constexpr int WAVE = 2 * BLOCK;
   static constexpr int SUMS = KS * R * T * 1024;
   static constexpr int SIZE = KS * WAVE > SUMS ? KS * WAVE : SUMS;
   static_assert(SIZE <= 160 * 1024, "LDS budget");
 };
 
-template <int TY, int R, int T, int KS, int U>
+template <int TY, int R, int T, int KS>
 __global__ __launch_bounds__(KS * 64) void k_fp8_decode(
     const uint8_t* __restrict__ X, const float* __restrict__ xs, const uint8_t* __restrict__ W,
     const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y,
     int M, int N, int K, int KB) {
-  using L = DecodeLds<R, T, KS, U>;
+  using L = DecodeLds<R, T, KS>;
   extern __shared__ __align__(16) int8_t smem[];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -85,43 +85,40 @@ __global__ __launch_bounds__(KS * 64) void k_fp8_decode(
   const uint32_t wbytes = (uint32_t)nrb * (uint32_t)KB * 2048u;
 
   struct Weights {
-    v4i w[U][R][2];
-    float s[U][R];
+    v4i w[R][2];
+    float s[R];
   };
-  // Loads of K blocks kb .. kb + U - 1 into registers and a stage of LDS.
-  // Blocks at or past KB get empty descriptors and zero scales, and the
-  // columns at or past K of a last block that K ends inside are read from an
-  // offset out of every range: zeros.  So a load has no branch and always the
-  // same OPS vector loads, which the wait in `step` counts.
-  constexpr int OPS = U * (2 * T + L::SDMA + 2 * R);
+  // Loads of K block kb into registers and a stage of LDS.  A block at or past
+  // KB gets empty descriptors and zero scales, and the columns at or past K of
+  // a last block that K ends inside are read from an offset out of every
+  // range: zeros.  So a load has no branch and always the same OPS vector
+  // loads, which the wait in `step` counts.
+  constexpr int OPS = 2 * T + L::SDMA + 2 * R;
   constexpr int kNonTemporal = 2;
   auto load = [&](int kb, int stage, Weights& o) {
+    const bool live = kb < KB;
+    const int k = live ? kb : 0;
+    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)X, (short)0, live ? (int)xbytes : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(xs + (size_t)k * M), (short)0, live ? M * 4 : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)W, (short)0, live ? (int)wbytes : 0, 0x00020000);
+    const bool out = (uint32_t)k * 128u + chunk * 16u >= (uint32_t)K;
+    int8_t* dst = mine + stage * L::BLOCK;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool live = kb + u < KB;
-      const int k = live ? kb + u : 0;
-      const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)X, (short)0, live ? (int)xbytes : 0, 0x00020000);
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(xs + (size_t)k * M), (short)0, live ? M * 4 : 0, 0x00020000);
-      const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)W, (short)0, live ? (int)wbytes : 0, 0x00020000);
-      const bool out = (uint32_t)k * 128u + chunk * 16u >= (uint32_t)K;
-      int8_t* dst = mine + (stage * U + u) * L::BLOCK;
+    for (int t = 0; t < 2 * T; ++t)
+      dma16(rx, dst + t * 1024, (int)(out ? kOutOfRange : xsrc[t]), k * 128);
 #pragma unroll
-      for (int t = 0; t < 2 * T; ++t)
-        dma16(rx, dst + t * 1024, (int)(out ? kOutOfRange : xsrc[t]), k * 128);
+    for (int t = 0; t < L::SDMA; ++t) dma4(rs, dst + T * 2048 + t * 256, lane * 4 + t * 256, 0);
 #pragma unroll
-      for (int t = 0; t < L::SDMA; ++t) dma4(rs, dst + T * 2048 + t * 256, lane * 4 + t * 256, 0);
+    for (int r = 0; r < R; ++r) {
+      o.s[r] = wsrow[r][k];  // block 0's past KB; `compute` takes zero there
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        o.s[u][r] = wsrow[r][k];  // block 0's past KB; `compute` takes zero there
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          o.w[u][r][h] = __builtin_bit_cast(
-              v4i, __builtin_amdgcn_raw_buffer_load_b128(
-                       rw, lane * 16, (int)(wsrc[r] + (uint32_t)k * 2048u + h * 1024u), kNonTemporal));
-      }
+      for (int h = 0; h < 2; ++h)
+        o.w[r][h] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                     rw, lane * 16, (int)(wsrc[r] + (uint32_t)k * 2048u + h * 1024u), kNonTemporal));
     }
   };
 
@@ -134,29 +131,26 @@ __global__ __launch_bounds__(KS * 64) void k_fp8_decode(
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   auto compute = [&](int kb, int stage, const Weights& o) {
+    const bool live = kb < KB;
+    const int8_t* src = mine + stage * L::BLOCK;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool live = kb + u < KB;
-      const int8_t* src = mine + (stage * U + u) * L::BLOCK;
+    for (int t = 0; t < T; ++t) {
+      const int8_t* row = src + (t * 16 + r16) * 128;
+      const v8i x = join(*reinterpret_cast<const v4i*>(row + (q4 ^ (r16 & 7)) * 16),
+                         *reinterpret_cast<const v4i*>(row + ((q4 + 4) ^ (r16 & 7)) * 16));
+      const float sx = *reinterpret_cast<const float*>(src + T * 2048 + (t * 16 + r16) * 4);
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const int8_t* row = src + (t * 16 + r16) * 128;
-        const v8i x = join(*reinterpret_cast<const v4i*>(row + (q4 ^ (r16 & 7)) * 16),
-                           *reinterpret_cast<const v4i*>(row + ((q4 + 4) ^ (r16 & 7)) * 16));
-        const float sx = *reinterpret_cast<const float*>(src + T * 2048 + (t * 16 + r16) * 4);
+      for (int r = 0; r < R; ++r) {
+        const float s = sx * (live ? o.s[r] : 0.0f);
+        const v4f p = mfma16_e4m3(join(o.w[r][0], o.w[r][1]), x);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float s = sx * (live ? o.s[u][r] : 0.0f);
-          const v4f p = mfma16_e4m3(join(o.w[u][r][0], o.w[u][r][1]), x);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[r][t][e] = fmaf(p[e], s, acc[r][t][e]);
-        }
+        for (int e = 0; e < 4; ++e) acc[r][t][e] = fmaf(p[e], s, acc[r][t][e]);
       }
     }
   };
-  // a step: the next K blocks' loads, then the wait for the current ones'
+  // a step: the next K block's loads, then the wait for the current one's
   auto step = [&](int kb, int stage, const Weights& cur, Weights& next) {
-    load(kb + KS * U, stage ^ 1, next);
+    load(kb + KS, stage ^ 1, next);
     wait_vm<OPS>();
     compute(kb, stage, cur);
     // the stage's reads are done before the next step's DMAs overwrite it
@@ -164,11 +158,11 @@ __global__ __launch_bounds__(KS * 64) void k_fp8_decode(
   };
 
   Weights a, b;
-  if (w * U < KB) {
-    load(w * U, 0, a);
-    for (int kb = w * U; kb < KB; kb += 2 * KS * U) {
+  if (w < KB) {
+    load(w, 0, a);
+    for (int kb = w; kb < KB; kb += 2 * KS) {
       step(kb, 0, a, b);
-      step(kb + KS * U, 1, b, a);
+      step(kb + KS, 1, b, a);
     }
   }
   wait_vm<0>();  // no DMA may still write LDS
@@ -200,10 +194,10 @@ __global__ __launch_bounds__(KS * 64) void k_fp8_decode(
   }
 }
 
-template <int TY, int R, int T, int KS, int U>
+template <int TY, int R, int T, int KS>
 static hipError_t run_decode(const Fp8Call& c, hipStream_t st) {
-  constexpr int SMEM = DecodeLds<R, T, KS, U>::SIZE;
-  auto kern = k_fp8_decode<TY, R, T, KS, U>;
+  constexpr int SMEM = DecodeLds<R, T, KS>::SIZE;
+  auto kern = k_fp8_decode<TY, R, T, KS>;
   // the dynamic-LDS limit is raised once per device the kernels run on
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
@@ -256,17 +250,17 @@ Fp8DecodePlan fp8_decode_plan(int M, int N) {
 template <int TY, int T>
 static hipError_t decode_blocks(int R, const Fp8Call& c, hipStream_t st) {
   constexpr int KS = T <= 4 ? 8 : 4;
-  if (R == 1) return run_decode<TY, 1, T, KS, 1>(c, st);
+  if (R == 1) return run_decode<TY, 1, T, KS>(c, st);
   if constexpr (T <= 7) {
-    if (R == 2) return run_decode<TY, 2, T, KS, 1>(c, st);
-    if (R == 5) return run_decode<TY, 5, T, 4, 1>(c, st);
+    if (R == 2) return run_decode<TY, 2, T, KS>(c, st);
+    if (R == 5) return run_decode<TY, 5, T, 4>(c, st);
   }
   if constexpr (T <= 6)
-    if (R == 3) return run_decode<TY, 3, T, KS, 1>(c, st);
+    if (R == 3) return run_decode<TY, 3, T, KS>(c, st);
   if constexpr (T <= 5)
-    if (R == 4) return run_decode<TY, 4, T, 4, 1>(c, st);
+    if (R == 4) return run_decode<TY, 4, T, 4>(c, st);
   if constexpr (T <= 4)
-    return R == 6 ? run_decode<TY, 6, T, 4, 1>(c, st) : run_decode<TY, 9, T, 4, 1>(c, st);
+    return R == 6 ? run_decode<TY, 6, T, 4>(c, st) : run_decode<TY, 9, T, 4>(c, st);
   return hipErrorInvalidValue;
 }
 
