@@ -288,10 +288,12 @@ __global__ __launch_bounds__((WM * WN + PW) * 64, 2) void k_fp8_gemm(
     for (int i = t; i < L::NBT * KS; i += (NWAVE + PW) * 64) sw[i] = i == t ? sw_first : weight_scale(i);
 
   if constexpr (DB) {
-    // 64 x 64 per wavefront: the registers hold all fragments of two K blocks.
-    // The next block's are read under the current one's MFMAs, which so never
-    // wait for LDS, and a K block needs one barrier: its stage is free as
-    // soon as the fragments are in registers.  Its DMAs run S - 1 blocks ahead.
+    // 256x128 and four-stage 128x128 tiles (64 tokens x 64 features per
+    // wavefront) and 64x128 tiles (64 x 32): the registers hold all fragments
+    // of two K blocks.  The next block's are read under the current one's
+    // MFMAs, which so never wait for LDS, and a K block needs one barrier: its
+    // stage is free as soon as the fragments are in registers.  Its DMAs run
+    // S - 1 blocks ahead.
     v8i fw[2][FN], fx[2][FM];
     float sx[2][FM], s_w[2];
     auto read = [&](int stage, int f, v8i(&gw)[FN], v8i(&gx)[FM]) {  // in the order of use
@@ -358,9 +360,10 @@ __global__ __launch_bounds__((WM * WN + PW) * 64, 2) void k_fp8_gemm(
       step(std::integral_constant<int, 1>{}, kb + 1);
     }
   } else {
-    // 64 x 128 per wavefront: the registers hold two weight fragments (the next
-    // feature block's loaded under the current one's MFMAs) and the tokens'
-    // FM fragments.  X and the two halves of W leave their stages separately,
+    // The two tiles with two stages, 256x256 (64 tokens x 128 features per
+    // wavefront) and 128x128 above one per CU (64 x 64; two workgroups share a
+    // CU): the registers hold two weight fragments (the next feature block's
+    // loaded under the current one's MFMAs) and the tokens' FM fragments.  X and the two halves of W leave their stages separately,
     // at two barriers per K block, so that their DMAs run S - 0.5 blocks ahead
     // in S stages (one barrier and S - 1.15 blocks: 4096x12288x49152 2066 us
     // against 1967).
