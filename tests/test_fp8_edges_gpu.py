@@ -202,3 +202,33 @@ def test_quantize_weight_large(K, N, dtype):
         assert torch.equal(ws[nb], (a / 448).float()), nb
         q = (t * (448 / a).float()[None, :, None]).view(n, KB * 128).to(E4M3)
         assert torch.equal(unpacked(w[cols], n, KB), q.view(torch.uint8)), nb
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_silu_mul_blocks_of_all_magnitudes(dtype):
+    """Blocks whose maximum lies at either side of 2^120 and of fp32's range,
+    next to ordinary blocks of the same rows: the gated products in 64 bits."""
+    rng = np.random.default_rng(8)
+    M, K = 37, 640
+    big = np.log2(float(torch.finfo(dtype).max))
+    gate = rng.uniform(-6, 6, (M, K))
+    up = rng.standard_normal((M, K))
+    for m in range(M):
+        for b in range(5):
+            c = b * 128 + int(rng.integers(128))  # one large product per block
+            lg, lu = (rng.uniform(0, big - 0.01, 2) if (m + b) % 3 else (1.0, 0.0))
+            gate[m, c], up[m, c] = 2.0 ** lg, rng.choice([-1, 1]) * 2.0 ** lu
+    GU = torch.from_numpy(np.concatenate([gate, up], 1)).to(dtype)
+    q, s = i8.fp8_silu_mul(GU.cuda())
+    y = F.silu_mul64(f32(GU))
+    s, v = s.cpu().numpy().astype(np.float64), F.e4m3_decode(raw(q))
+    a = np.abs(y).reshape(M, 5, 128).max(2).T
+    inside, past = a < (1 - 2.0 ** -20) * 2.0 ** 128, a > (1 + 2.0 ** -20) * 2.0 ** 128
+    assert np.all(np.abs(s - a / 448)[inside] <= (GATE + 2.0 ** -24) * a[inside] / 448)
+    assert np.all(np.isinf(s[past]))
+    ok = np.repeat(inside.T, 128, 1)
+    want = y / np.repeat(np.where(inside, s, 1.0).T, 128, 1)
+    tol = np.maximum(np.abs(want) * 2.0 ** -4, 2.0 ** -10) + (2 * GATE + 2.0 ** -22) * np.abs(want)
+    assert np.all((np.abs(v - want) <= tol)[ok])
+    if dtype == torch.bfloat16:
+        assert past.any() and (inside & (a > 2.0 ** 120)).any()
