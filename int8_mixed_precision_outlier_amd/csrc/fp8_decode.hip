@@ -16,8 +16,10 @@
 // block is on its way under the MFMAs and scaling fmas of the current one.
 //
 // Bound by HBM for a few tokens (1x12288x49152: 86 us = 7.0 TB/s, 32x12288x36864:
-// 71 us = 6.4 TB/s), by what a CU takes in of both operands (about 55 GB/s)
-// towards 128.
+// 71 us = 6.4 TB/s).  Towards 128 tokens no unit is the bound: on 77x5136x20464
+// (29 us, 3.6 TB/s of weight, 28 GB/s of both operands per CU) the one wavefront
+// per SIMD issues 35 % of its time, waits for memory 36 % and for its turn or
+// the matrix unit 29 %, and the matrix unit is busy 14 % of it (counters).
 #include "common.hpp"
 #include "fp8.hpp"
 #include "launch.hpp"
@@ -215,11 +217,11 @@ static hipError_t run_decode(const Fp8Call& c, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Feature blocks per workgroup.  A CU takes in a bounded rate of operands, so
-// the time goes with the most loaded CU's rounds of workgroups times the
-// blocks it reads per K block in each, R of the weight and T of the tokens;
-// the choice that makes that least (ties: fewer) is the fastest or within 4 %
-// of it at 28 measured shapes of 9 to 128 tokens (32x5120x5120, R = 1, 2, 3, 4,
+// Feature blocks per workgroup.  The time goes about with the most loaded CU's
+// rounds of workgroups times the blocks it reads per K block in each, R of the
+// weight and T of the tokens; among the counts that are built, the choice that
+// makes that least (ties: fewer) is the fastest or within 4 % of it at 28
+// measured shapes of 9 to 128 tokens (32x5120x5120, R = 1, 2, 3, 4,
 // 5: 12.0, 9.3, 11.2, 12.9, 13.6 us; 64x12288x36864, R = 1, 3, 5, 9: 155.6,
 // 95.8, 86.9, 75.9; 128x5120x5120, R = 1, 2, 3: 26.6, 17.8, 21.1).  At most 8
 // tokens bring little token traffic (the rows past M repeat the last one):
@@ -228,7 +230,11 @@ static hipError_t run_decode(const Fp8Call& c, hipStream_t st) {
 // tokens the partial sums of more than 5 blocks would not fit LDS, and where 1
 // to 4 blocks and the tokens' make more than 9, 64x128 tiles are faster
 // (120x5120x16384, 4 blocks: 27.3 us against 23.6), above 112 tokens tiles
-// also where 5 would be best.
+// also where 5 would be best.  7 and 8 are not built: they would gain where they
+// just fill the CUs, near 28672 and 32768 features (weights that no cache
+// holds, us as it is / with them: 16x8192x28672 40.2 / 38.7, 32x12288x28672 60.6 /
+// 56.9, 48x4096x28672 25.3 / 23.8, 64x8192x28672 48.0 / 43.5, 32x5120x32000 30.0 /
+// 29.5, 64x12288x32768 72.5 / 69.8).
 constexpr int kDecodeR[] = {1, 2, 3, 4, 5, 6, 9};
 
 Fp8DecodePlan fp8_decode_plan(int M, int N) {

@@ -98,15 +98,16 @@ __global__ __launch_bounds__((WM * WN + PW) * 64, 2) void k_fp8_gemm(
   constexpr int NWAVE = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int FM = WTM / 16, FN = WTN / 16;
-  // 1 KB DMAs of a wavefront per K block: of X, of either half of W, and of
-  // its token scales
   // PW > 0: the last PW wavefronts only issue the DMAs, the others compute.  A
   // wavefront that issues waits for the address unit, 16 cycles per DMA; where
   // one wavefront per SIMD computes, nothing else would use that time
   // (256x5120x5120 on 64x128 tiles: 18.4 us with the DMAs in the computing
-  // wavefronts, 15.8 with four more, both with three stages; 1024x4096x4096 on
-  // 128x128 tiles: 21.4 in eight computing ones, 19.2 in four more beside four).
+  // wavefronts, 15.8 with four more, both with three stages; 128x128 tiles, in
+  // eight computing ones / in four more beside four, calls in a graph:
+  // 1024x4096x4096 22.8 / 21.0, 512x5120x5120 23.3 / 21.4, 512x5120x8192 28.1 / 25.0).
   constexpr int DW = PW > 0 ? PW : NWAVE;  // wavefronts that share the DMAs
+  // 1 KB DMAs of a wavefront per K block: of X, of either half of W, and of
+  // its token scales
   constexpr int XDMA = BM / 8 / DW, HDMA = BN / 16 / DW, SDMA = PW > 0 ? 1 : WTM / 64;
   static_assert(BN / 16 % DW == 0 && BM / 8 % DW == 0 && WTM % 64 == 0, "DMA split");
   constexpr int SROW = PW > 0 ? BM : NWAVE * WTM;  // token scales of a stage
@@ -514,6 +515,16 @@ static hipError_t run_tiles(int cfg, const Fp8Call& c, int nbase, int nend, hipS
 //            20.1 / 20.7, 120x5120x16384 27.3 / 23.6, but 120x12288x12288 45.2 /
 //            48.9; with weights in the last-level cache 104x5120x12288 22.9 /
 //            15.1; 128x12288x49152: 161 against 144 on 128x128 tiles).
+// Up to 64 tokens the decode kernel runs whatever the costs.  Fitted above
+// that, they would put tiles in its place where one per CU just fills the chip
+// (64x128 tiles near 32768 features, 128x128 near 65536).  With weights that no
+// cache holds (decode / tiles, us) that loses up to 32 tokens: 1x12288x28672
+// 52.8 / 61.4, 8x5120x20480 19.1 / 20.9, 16x8192x28672 40.0 / 42.4, 32x12288x32768
+// 65.7 / 71.5, 4x5120x51200 42.8 / 52.5 (32x5120x25600 25.9 / 25.3); towards 64
+// it would gain at most of these sizes: 64x5120x26000 32.0 / 27.9, 56x5120x28672
+// 32.4 / 28.7, 64x12288x28672 68.4 / 67.3, 64x4096x32768 29.3 / 27.7, 64x5120x51200
+// 64.3 / 57.1, 64x12288x57344 143.2 / 136.9, but 64x5120x24576 26.3 / 27.4,
+// 40x5120x51200 53.2 / 54.9.
 // When 256x256 tiles would leave the last round partly empty, the features
 // can be split: [0, n1) in whole rounds of 256x256 tiles, [n1, N) in a second
 // launch of smaller tiles (kGap for its fill and drain, taken when it saves

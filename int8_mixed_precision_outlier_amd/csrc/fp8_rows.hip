@@ -40,14 +40,16 @@ __device__ __forceinline__ uint2 quant8(const float (&y)[8], float& scale) {
 // correction for what t = -g log2(e) loses in its rounding (and log2(e) in
 // its own), and the quotient is a product with the reciprocal instruction's
 // result, at a third of the instructions of expf and the IEEE division, which
-// bound this kernel (2048x20480 with two blocks per group: 37.9 us; with expf
+// bound this kernel (2048x20480 with two blocks per group: 38.2 us; with expf
 // and four: 50.8).  Within 8 half steps of 2^-24: the exponential and the
 // reciprocal instruction 2 each, the correction (second-order terms and the
 // rest of log2(e) add 2^-34), its fma to 1 + exp(-g) and the last two products
 // 1 each.  The reciprocal is taken of (1 + exp(-g)) / 256 and the gate divided
 // by 256, both exact: below g = -87.33 that of 1 + exp(-g) would leave the
 // normal numbers, where the instruction gives 0, and so would y though a bf16
-// u can be 3e38 (the gate's scaling costs 3 %, 2048x20480 bf16 36.8 -> 38.2 us).
+// u can be 3e38.  The gate's scaling costs 2 to 4 % (2048x20480 fp16 36.7 ->
+// 38.2 us, 4096x12288 bf16 43.6 -> 44.6, calls in a graph); taken back per block
+// behind a branch for products past 2^120 it cost as much.
 // From g = -88.73 on exp(-g) is infinite and y a signed zero.
 // The exponent's argument stops at 200, where exp is infinite or nothing
 // beside 1 already, so that no product with log2(e) leaves the range: t and r
@@ -273,8 +275,8 @@ static hipError_t run_strips(const void* X, int M, int K, void* Xq, float* xs, h
 // One block per 16 lanes while that keeps the workgroups within one round of
 // the chip (8 per CU): the calls are then bound by latency (1x20480 gated, U =
 // 1, 2, 4: 2.5, 3.1, 4.0 us; 300x5120: 2.5, 2.8, 3.4).  Two for more: 4096x12288,
-// U = 1, 2, 4, 8: 27.4, 24.9, 25.1, 27.1 us (6.1 TB/s); 2048x20480 gated: 38.6,
-// 37.9, 38.2, 41.5 (5.6 TB/s).
+// U = 1, 2, 4, 8: 27.4, 24.9, 25.1, 27.1 us (6.1 TB/s); 2048x20480 gated: 38.8,
+// 38.2, 38.8, 41.7 (5.5 TB/s).
 template <int T, bool GATED>
 static hipError_t run_blocks(const void* X, int M, int K, void* Xq, float* xs, hipStream_t st) {
   const int64_t groups = ((int64_t)M + 15) / 16 * ((K + kFp8Block - 1) / kFp8Block);
