@@ -232,3 +232,47 @@ def test_silu_mul_blocks_of_all_magnitudes(dtype):
     assert np.all((np.abs(v - want) <= tol)[ok])
     if dtype == torch.bfloat16:
         assert past.any() and (inside & (a > 2.0 ** 120)).any()
+
+
+@pytest.mark.parametrize("M,N", [(1, 1 << 24), (128, (1 << 24) - 16), (1 << 27, 16), ((1 << 26) - 5, 32)])
+def test_matmul_most_features_and_tokens(M, N):
+    """The largest counts of features and of tokens that K = 16 allows: the
+    first, middle and last ones, exactly."""
+    K = 16
+    x, w = integers(M, K, 5), integers(N, K, 6)
+    ones = lambda *s: torch.ones(s, device="cuda")  # noqa: E731
+    Y = i8.fp8_matmul(x.view(E4M3), ones(1, M), i8.fp8_pack_weight(w.view(E4M3)), ones(-(-N // 128), 1),
+                      out_dtype=torch.float16)
+    for m in (slice(0, 300), slice(M // 2, M // 2 + 300), slice(max(0, M - 300), M)):
+        for n in (slice(0, 300), slice(N // 2, N // 2 + 300), slice(max(0, N - 300), N)):
+            want = F.e4m3_decode(raw(x[m])) @ F.e4m3_decode(raw(w[n])).T
+            assert np.array_equal(Y[m, n].cpu().numpy(), want.astype(np.float16)), (m, n)
+    del x, w, Y
+    torch.cuda.empty_cache()
+
+
+def test_capture_on_a_given_stream():
+    """Calls captured on the stream that they are given, with temporaries that
+    are dropped inside: every replay gives what eager calls give."""
+    K, N, M = 528, 272, 40
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, w, weight = rnd(M, K), i8.fp8_quantize_weight(rnd(K, 2 * N)), rnd(K)
+
+    def chain(stream):
+        q, s, h = i8.fp8_rms_norm(x, weight, residual=x, stream=stream)
+        gu = i8.fp8_matmul(q, s, *w, stream=stream)
+        del q, s
+        return h, *i8.fp8_silu_mul(gu, stream=stream)
+    stream = torch.cuda.Stream()
+    chain(stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = chain(stream)
+    for k in range(4):
+        x.copy_(rnd(M, K))
+        graph.replay()
+        want = chain(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(out, want)), k
