@@ -432,6 +432,30 @@ int fp8_rms_norm(const void *X, const void *residual, const void *weight,
                  void *X_f8, float *x_scale, hipStream_t stream);
 
 /*
+ * fp8_sandwich_norm -- the norm after a block, the residual's addition and
+ * the norm before the next block, in one pass:
+ *     z = X / sqrt(mean(X^2) + eps) * post_weight
+ *     h = residual_scale * residual + gate * z
+ *     y = h / sqrt(mean(h^2) + eps) * pre_weight
+ * all in fp32 and none of it rounded in between; then h is rounded to H, and
+ * y either quantized into X_f8, x_scale (as by fp8_quantize) or rounded to Y.
+ *   X, residual  in  [M][K]: the block's output and the stream it is added to.
+ *   post_weight, pre_weight  in  [K].
+ *   gate         in  [gate_rows][K], M % gate_rows == 0: row g is that of the
+ *                    tokens g * M / gate_rows and on (1: one for all, M: one
+ *                    each).  NULL, with gate_rows 0: none.
+ *   residual_scale   finite.
+ *   eps          in  > 0, finite.
+ *   H            out [M][K]; may be the residual's or X's own buffer.
+ *   Y, or X_f8 with x_scale  out; the other NULL.
+ * A row whose sum of squares passes fp32's range becomes 0, as in fp8_rms_norm.
+ */
+int fp8_sandwich_norm(const void *X, const void *residual, const void *post_weight,
+                      const void *pre_weight, const void *gate, int64_t gate_rows,
+                      float residual_scale, int type, int64_t M, int64_t K, float eps,
+                      void *H, void *Y, void *X_f8, float *x_scale, hipStream_t stream);
+
+/*
  * fp8_silu_mul -- the gated activation before a feed-forward's second
  * product: gate_up [M][2K] (16-bit; a row is its K gates, then its K ups) ->
  * the quantized g / (1 + exp(-g)) * u, in fp32 up to the quantizer.  Finite
@@ -470,6 +494,76 @@ int fp8_matmul(const void *X_f8, const float *x_scale, int64_t M, int64_t K,
  *     features [0, n1) in 256x256 tiles, [n1, N) in smaller ones of 128 columns.
  */
 int fp8_matmul_config(int64_t M, int64_t N, int64_t K, int32_t *cfg);
+
+/*
+ * ---- Mixture of experts ----------------------------------------------
+ *
+ * The router, and the experts' gated feed-forward for few tokens, from
+ * block-scaled e4m3 weights and 16-bit activations.  A token has top_k places;
+ * place j of token m is the pair m * top_k + j.
+ */
+#define INT8MM_MAX_EXPERTS 1024
+#define INT8MM_MAX_TOP_K 32
+#define INT8MM_ROUTE_MAX_TOKENS (1 << 18) /* M of one moe_route call */
+#define INT8MM_MOE_MAX_PAIRS 8192 /* M * top_k of one fp8_moe call */
+
+/* Workspace bytes of moe_route; 0 if the sizes are invalid (and for M == 0). */
+size_t moe_route_workspace_size(int64_t M, int64_t K, int64_t E, int64_t top_k);
+
+/*
+ * moe_route -- each token's top_k experts and their weights:
+ *     p = softmax over the experts of X . W^T
+ *     experts = the top_k largest logits in descending order, ties to the
+ *               lower index;  weights = their p, or with `normalize` p / sum(p)
+ *   X        in  [M][K], W in [E][K], 16-bit of one type.
+ *   experts  out [M][top_k] int32, weights out [M][top_k] fp32.
+ * The order is that of logits summed in 64 bits.  A NaN logit ranks with -inf and
+ * makes all of its token's weights NaN; the experts are distinct and in range
+ * whatever the logits.
+ *   workspace    device, 256-byte aligned, moe_route_workspace_size bytes, no
+ *                initial contents required.
+ * K % 16 == 0, M <= INT8MM_ROUTE_MAX_TOKENS, M * K <= INT8MM_MAX_MN, 1 <=
+ * top_k <= E, X and W 16-byte aligned.  M == 0 is a no-op; K == 0 makes all
+ * logits 0.
+ */
+int moe_route(const void *X, const void *W, int type, int64_t M, int64_t K, int64_t E,
+              int64_t top_k, int normalize, int32_t *experts, float *weights,
+              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of fp8_moe; 0 if the sizes are invalid (and where none is needed). */
+size_t fp8_moe_workspace_size(int64_t M, int64_t K, int64_t I, int64_t E, int64_t top_k);
+
+/*
+ * fp8_moe -- the experts of each token:
+ *     a[p] = silu(X[m] . G_e^T) * (X[m] . U_e^T)    for the pairs p = (m, j), e = experts[p]
+ *     Y[m] = sum over j of weights[p] * (a[p] . D_e^T)
+ * with fp32 sums, the pairs of a token added in the order of j, rounded once.
+ * Each expert that some token has is read once for (up to 64 of) its tokens,
+ * so the call is made for few tokens per expert.
+ *   X              in  [M][K], 16-bit, Y out [M][K] of the same type.
+ *   experts        in  [M][top_k] int32.  A pair whose expert is not in
+ *                      0 .. E-1 (such as -1 for an empty place) contributes
+ *                      nothing; a token may have an expert twice.
+ *   weights        in  [M][top_k] fp32.
+ *   gate_up_f8     in  the E packed matrices [2I][K] one after another (a
+ *                      matrix's rows are its I gates, then its I ups), each
+ *                      fp8_packed_size(2I, K) bytes as fp8_quantize_weight or
+ *                      fp8_pack_weight leaves it;
+ *   gate_up_scale  in  [E][ceil(2I/128)][ceil(K/128)].
+ *   down_f8        in  the E packed matrices [K][I];
+ *   down_scale     in  [E][ceil(K/128)][ceil(I/128)].
+ *   workspace          device, 256-byte aligned, fp8_moe_workspace_size bytes,
+ *                      no initial contents required.
+ * K % 16 == 0, I % 16 == 0, 1 <= E <= INT8MM_MAX_EXPERTS, 1 <= top_k <=
+ * INT8MM_MAX_TOP_K, M * top_k <= INT8MM_MOE_MAX_PAIRS, one expert's matrices
+ * within fp8_packed_size's range.  M == 0 or K == 0 is a no-op; I == 0
+ * writes zeros.
+ */
+int fp8_moe(const void *X, int type, int64_t M, int64_t K, const int32_t *experts,
+            const float *weights, int64_t top_k, const void *gate_up_f8,
+            const float *gate_up_scale, const void *down_f8, const float *down_scale,
+            int64_t I, int64_t E, void *Y, void *workspace, size_t workspace_bytes,
+            hipStream_t stream);
 
 /*
  * Profiling aid (not thread-safe; for benchmarks).  While enabled, every

@@ -26,7 +26,8 @@ __all__ = [
     "kernel_config", "outlier_cache_size", "build_outlier_cache", "mixed_matmul_cached",
     "STATUS_OK", "STATUS_EINVAL", "STATUS_EALIGN", "STATUS_EWORKSPACE", "STATUS_EHIP",
     "FP8_BLOCK", "fp8_kpad", "fp8_pack_weight", "fp8_quantize_weight", "fp8_quantize",
-    "fp8_rms_norm", "fp8_silu_mul", "fp8_matmul", "fp8_matmul_config",
+    "fp8_rms_norm", "fp8_sandwich_norm", "fp8_silu_mul", "fp8_matmul", "fp8_matmul_config",
+    "moe_route", "fp8_moe", "fp8_pack_experts", "fp8_quantize_experts", "MOE_MAX_PAIRS",
     "STATUS_ESCRATCH", "FLAG_OVERFLOW", "FLAG_CACHE_MISS", "FLAG_CACHE_MISMATCH",
 ]
 
@@ -115,6 +116,19 @@ def load() -> ctypes.CDLL:
     lib.fp8_matmul.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _vp]
     lib.fp8_matmul_config.restype = ctypes.c_int
     lib.fp8_matmul_config.argtypes = [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_int32)]
+    lib.fp8_sandwich_norm.restype = ctypes.c_int
+    lib.fp8_sandwich_norm.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, ctypes.c_float, _i32, _i64, _i64,
+                                      ctypes.c_float, _vp, _vp, _vp, _vp, _vp]
+    lib.moe_route_workspace_size.restype = ctypes.c_size_t
+    lib.moe_route_workspace_size.argtypes = [_i64] * 4
+    lib.moe_route.restype = ctypes.c_int
+    lib.moe_route.argtypes = [_vp, _vp, _i32, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _vp,
+                              ctypes.c_size_t, _vp]
+    lib.fp8_moe_workspace_size.restype = ctypes.c_size_t
+    lib.fp8_moe_workspace_size.argtypes = [_i64] * 5
+    lib.fp8_moe.restype = ctypes.c_int
+    lib.fp8_moe.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64,
+                            _vp, _vp, ctypes.c_size_t, _vp]
     _lib = lib
     return lib
 
@@ -502,4 +516,6 @@ def timing_read():
 
 
 from .fp8 import (FP8_BLOCK, fp8_kpad, fp8_matmul, fp8_matmul_config, fp8_pack_weight,  # noqa: E402
-                  fp8_quantize, fp8_quantize_weight, fp8_rms_norm, fp8_silu_mul)
+                  fp8_quantize, fp8_quantize_weight, fp8_rms_norm, fp8_sandwich_norm, fp8_silu_mul)
+from .moe import (MOE_MAX_PAIRS, fp8_moe, fp8_pack_experts, fp8_quantize_experts,  # noqa: E402
+                  moe_route)

@@ -39,7 +39,6 @@ EventPair* timing_slot() {
   return &g_events[g_events_used++];
 }
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 int hip_status(hipError_t e) {

@@ -20,4 +20,12 @@ int run_mixed(const void* X_f16, int64_t M, int64_t K, const int8_t* W_i8,
 // int8mm_last_hip_error and returns INT8MM_EHIP.
 int hip_error_status(hipError_t e);
 
+// Argument checks shared by the e4m3 and the mixture-of-experts functions.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Type, sizes and alignment of a rows x K matrix (`width` columns are stored
+// per row of the input: K, or 2K for a gated pair).
+int check_rows(int type, int64_t rows, int64_t K, int64_t width);
+// Sizes of an N x K e4m3 weight.
+int check_weight(int64_t K, int64_t N);
+
 }  // namespace i8mm

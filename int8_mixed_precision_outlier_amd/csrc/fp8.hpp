@@ -101,6 +101,17 @@ hipError_t launch_fp8_silu_mul(const void* GU, int type, int M, int I, void* Aq,
                                hipStream_t st);
 hipError_t launch_fp8_rms_norm(const void* X, const void* R, const void* g, int type, int M, int K,
                                float eps, void* H, void* Xq, float* xs, hipStream_t st);
+// One call of the norms on both sides of a residual's addition; pointers as in
+// include/int8mm.h (gate null: none; Y null: quantized into Xq, xs).
+struct SandwichCall {
+  const uint16_t *X, *R, *post, *pre, *gate;
+  uint16_t *H, *Y;
+  uint8_t* Xq;
+  float* xs;
+  int M, K, tokens_per_gate, type;
+  float alpha, eps;
+};
+hipError_t launch_sandwich_norm(const SandwichCall& c, hipStream_t st);
 hipError_t launch_fp8_quantize_weight(const void* W, int type, int K, int N, void* Wq, float* ws,
                                       hipStream_t st);
 hipError_t launch_fp8_pack_weight(const void* src, int N, int K, void* dst, hipStream_t st);

@@ -9,12 +9,8 @@
 
 using namespace i8mm;
 
-namespace {
+namespace i8mm {
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Type, sizes and alignment of a rows x K matrix (`width` columns are stored
-// per row of the input: K, or 2K for a gated pair).
 int check_rows(int type, int64_t rows, int64_t K, int64_t width) {
   if (type != INT8MM_F16 && type != INT8MM_BF16) return INT8MM_EINVAL;
   if (rows < 0 || K < 0 || K > INT8MM_MAX_K || rows > INT8MM_MAX_MN) return INT8MM_EINVAL;
@@ -30,7 +26,7 @@ int check_weight(int64_t K, int64_t N) {
   return K % 16 != 0 || N % 16 != 0 ? INT8MM_EALIGN : INT8MM_OK;
 }
 
-}  // namespace
+}  // namespace i8mm
 
 extern "C" {
 
@@ -81,6 +77,30 @@ int fp8_rms_norm(const void* X, const void* residual, const void* weight, int ty
     return INT8MM_EALIGN;
   return hip_error_status(launch_fp8_rms_norm(X, residual, weight, type, (int)M, (int)K, eps, H,
                                               X_f8, x_scale, stream));
+}
+
+int fp8_sandwich_norm(const void* X, const void* residual, const void* post_weight,
+                      const void* pre_weight, const void* gate, int64_t gate_rows,
+                      float residual_scale, int type, int64_t M, int64_t K, float eps, void* H,
+                      void* Y, void* X_f8, float* x_scale, hipStream_t stream) {
+  const int st = check_rows(type, M, K, K);
+  if (st != INT8MM_OK) return st;
+  if (!(eps > 0.0f) || isinf(eps) || !isfinite(residual_scale)) return INT8MM_EINVAL;
+  if (gate_rows < 0 || !gate != !gate_rows) return INT8MM_EINVAL;
+  if (gate_rows > 0 && M % gate_rows != 0) return INT8MM_EINVAL;
+  if (M == 0 || K == 0) return INT8MM_OK;
+  if (!X || !residual || !post_weight || !pre_weight || !H) return INT8MM_EINVAL;
+  if (!X_f8 != !x_scale || !Y == !X_f8) return INT8MM_EINVAL;
+  if (!aligned16(X) || !aligned16(residual) || !aligned16(post_weight) || !aligned16(pre_weight) ||
+      !aligned16(gate) || !aligned16(H) || !aligned16(Y) || !aligned16(X_f8) ||
+      !aligned16(x_scale))
+    return INT8MM_EALIGN;
+  const auto in = [](const void* p) { return static_cast<const uint16_t*>(p); };
+  const SandwichCall c{in(X), in(residual), in(post_weight), in(pre_weight), in(gate),
+                       static_cast<uint16_t*>(H), static_cast<uint16_t*>(Y),
+                       static_cast<uint8_t*>(X_f8), x_scale, (int)M, (int)K,
+                       (int)(gate ? M / gate_rows : 1), type, residual_scale, eps};
+  return hip_error_status(launch_sandwich_norm(c, stream));
 }
 
 int fp8_silu_mul(const void* gate_up, int type, int64_t M, int64_t K, void* A_f8, float* a_scale,

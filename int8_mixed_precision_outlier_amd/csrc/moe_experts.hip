@@ -1,0 +1,400 @@
+// A mixture of experts' gated feed-forward for few tokens (gfx950), from
+// block-scaled e4m3 weights and 16-bit activations:
+//   a[p]  = silu(x . G_e^T) * (x . U_e^T)     for each pair p of a token and its expert e
+//   y[m]  = sum over the token's pairs of weight[p] * (a[p] . D_e^T)
+//
+// Few tokens are bound by the stream of the chosen experts' weights, so each
+// chosen expert is read once for all its tokens, and the activations stay in 16
+// bits: quantizing them would not shorten the stream.  The e4m3 numbers become
+// fp16 or bf16 in registers (exactly) and meet the tokens in 16x16x32 matrix
+// instructions; the sum of a 128-column block is scaled once in fp32.  The
+// gated product between the two kernels keeps 16 bits of mantissa as a sum of
+// two bf16 numbers, which feed two matrix instructions each: one bf16 number
+// would add as much error as the result's own rounding, and an fp16 one could
+// overflow.
+#include "fp8.hpp"
+#include "fp8_quant.hpp"
+#include "launch.hpp"
+#include "moe.hpp"
+
+namespace i8mm {
+
+namespace {
+
+// A row offset past every operand (at most 2^31 bytes), with room below 2^32
+// for the offsets inside a block.
+constexpr uint32_t kNoRow = 0xfffff000u;
+
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+// 16x16x32 matrix instruction on fp16 or bf16 operands (lane convention as
+// mfma16_f16).
+template <int TY>
+__device__ __forceinline__ v4f mfma32(v4i a, v4i b, v4f c) {
+  if constexpr (TY == kF16)
+    return mfma16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a),
+                                                   __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+}
+
+// Two e4m3 numbers (the low or high half of a dword) as fp16 or bf16, exactly.
+template <int TY, bool HIGH>
+__device__ __forceinline__ int widen2(int w) {
+  if constexpr (TY == kF16)
+    return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH));
+  else
+    return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
+}
+
+// A lane's 16 e4m3 numbers of a half block as two matrix operands.
+template <int TY>
+__device__ __forceinline__ void widen16(const v4i& w, v4i (&o)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    o[i] = v4i{widen2<TY, false>(w[2 * i]), widen2<TY, true>(w[2 * i]),
+               widen2<TY, false>(w[2 * i + 1]), widen2<TY, true>(w[2 * i + 1])};
+}
+
+// The expert of slot s: the experts in turn, or, where there are fewer pairs
+// than experts, that of pair s if s is the expert's first pair.  -1: none.
+// Writes the expert's pairs to `list` in ascending order and their number to n.
+template <int NT>
+__device__ __forceinline__ int expert_of_slot(const MoeCall& c, int s, uint16_t* list, int* counts,
+                                              int& n) {
+  const int P = c.M * c.top_k;
+  int e = P < c.E ? c.experts[s] : s;
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  constexpr int NW = NT / 64;
+  // each wavefront counts its part of the pairs, then writes it behind the others'
+  const int seg = ((P + NW - 1) / NW + 63) & ~63;
+  const int lo = w * seg, hi = min(P, lo + seg);
+  int mine = 0;
+  for (int p = lo + lane; p - lane < hi; p += 64)
+    mine += __builtin_popcountll(__ballot(p < hi && c.experts[p] == e));
+  if (lane == 0) counts[w] = mine;
+  __syncthreads();
+  int at = 0;
+  n = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    if (i < w) at += counts[i];
+    n += counts[i];
+  }
+  for (int p = lo + lane; p - lane < hi; p += 64) {
+    const bool is = p < hi && c.experts[p] == e;
+    const uint64_t b = __ballot(is);
+    if (is) list[at + __builtin_popcountll(b & ((1ull << lane) - 1))] = (uint16_t)p;
+    at += __builtin_popcountll(b);
+  }
+  __syncthreads();
+  n = __builtin_amdgcn_readfirstlane(n);
+  if ((unsigned)e >= (unsigned)c.E || n == 0 || (P < c.E && list[0] != s)) return -1;
+  return e;
+}
+
+// One product of NB blocks of 16 weight rows with T blocks of 16 tokens over
+// the wavefront's K blocks w, w + KS, ...
+//   w_row[b]   row block of the expert's packed matrix
+//   rows[t]    byte offset of the lane's token in the operand, or kNoRow
+// The operand holds `PLANES` numbers per column that are added: 16 columns are
+// 32 bytes of the first, then 32 of the second.
+template <int TY, int NB, int T, int PLANES, int KS>
+struct Product {
+  struct Stage {
+    v4i w[NB][2];
+    v4i x[T][2][PLANES][2];
+    float s[NB];
+  };
+  typedef const __attribute__((address_space(4))) float* scalar_ptr;
+  const uint8_t* W;
+  uint32_t w_bytes;
+  uint32_t w_at[NB];
+  scalar_ptr s_at[NB];
+  const void* X;
+  uint32_t x_bytes;
+  uint32_t rows[T];
+  int K, KB, lane, q4;
+
+  __device__ __forceinline__ void load(int kb, Stage& o) const {
+    constexpr int kNonTemporal = 2;
+    const bool live = kb < KB;
+    const int k = live ? kb : 0;
+    const __amdgpu_buffer_rsrc_t rw =
+        __builtin_amdgcn_make_buffer_rsrc((void*)W, (short)0, live ? (int)w_bytes : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rx =
+        __builtin_amdgcn_make_buffer_rsrc((void*)X, (short)0, live ? (int)x_bytes : 0, 0x00020000);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      o.s[b] = s_at[b][k];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        o.w[b][h] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                     rw, lane * 16, (int)(w_at[b] + (uint32_t)k * 2048u + h * 1024u), kNonTemporal));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool out = k * 128 + h * 64 + q4 * 16 >= K;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const uint32_t at = (out ? kNoRow : rows[t]) + h * 128 * PLANES;
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            o.x[t][h][p][i] = __builtin_bit_cast(
+                v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                         rx, (int)(at + p * 32 + i * 16), k * (256 * PLANES), 0));
+      }
+    }
+  }
+
+  __device__ __forceinline__ void compute(const Stage& s, v4f (&acc)[NB][T]) const {
+    v4f sum[NB][T];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int t = 0; t < T; ++t) sum[b][t] = v4f{};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        v4i w[2];
+        widen16<TY>(s.w[b][h], w);
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sum[b][t] = mfma32<TY>(w[i], s.x[t][h][p][i], sum[b][t]);
+      }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[b][t][e] = fmaf(sum[b][t][e], s.s[b], acc[b][t][e]);
+  }
+
+  __device__ __forceinline__ void run(int w, v4f (&acc)[NB][T]) const {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int t = 0; t < T; ++t) acc[b][t] = v4f{};
+    if (w >= KB) return;
+    Stage a, b;
+    load(w, a);
+    for (int kb = w; kb < KB; kb += 2 * KS) {
+      load(kb + KS, b);
+      compute(a, acc);
+      if (kb + KS >= KB) break;
+      load(kb + 2 * KS, a);
+      compute(b, acc);
+    }
+  }
+};
+
+// The sums of the wavefronts' partial products, in wavefront order; `red` is
+// [KS][NB * T][64] v4f of LDS.  Leaves tile o = b * T + t with any wavefront.
+template <int NB, int T, int KS>
+__device__ __forceinline__ void spread_partials(const v4f (&acc)[NB][T], int w, int lane, v4f* red) {
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int t = 0; t < T; ++t) red[(w * NB * T + b * T + t) * 64 + lane] = acc[b][t];
+  __syncthreads();
+}
+template <int NB, int T, int KS>
+__device__ __forceinline__ v4f joined(const v4f* red, int o, int lane) {
+  v4f y = red[o * 64 + lane];
+#pragma unroll
+  for (int i = 1; i < KS; ++i) y += red[(i * NB * T + o) * 64 + lane];
+  return y;
+}
+
+// First product: workgroup (f, s) makes 16 features of the gated product, gate
+// and up rows side by side, for all tokens of slot s's expert.
+template <int TY, int T, int KS>
+__device__ __forceinline__ void up_tokens(const MoeCall& c, int e, int j0, int n,
+                                          const uint16_t* list, v4f* red) {
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q4 = lane >> 4, r16 = lane & 15;
+  const int f = blockIdx.x;
+  using P = Product<TY, 2, T, 1, KS>;
+  P p;
+  p.K = c.K;
+  p.KB = (c.K + kFp8Block - 1) / kFp8Block;
+  p.lane = lane;
+  p.q4 = q4;
+  p.w_bytes = (uint32_t)(2 * c.I) * (uint32_t)(p.KB * kFp8Block);
+  p.W = c.up + (size_t)e * p.w_bytes;
+  const float* scales = c.up_scale + (size_t)e * ((2 * c.I + 127) / 128) * p.KB;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int rb = b * (c.I / 16) + f;
+    p.w_at[b] = (uint32_t)rb * (uint32_t)p.KB * 2048u;
+    p.s_at[b] = (typename P::scalar_ptr)(uintptr_t)(scales + (size_t)(rb / 8) * p.KB);
+  }
+  p.X = c.X;
+  p.x_bytes = (uint32_t)c.M * (uint32_t)c.K * 2u;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int j = j0 + t * 16 + r16;
+    p.rows[t] = j < n ? (uint32_t)(list[j] / c.top_k) * (uint32_t)c.K * 2u + q4 * 32u : kNoRow;
+  }
+  v4f acc[2][T];
+  p.run(w, acc);
+  spread_partials<2, T, KS>(acc, w, lane, red);
+  for (int t = w; t < T; t += KS) {
+    const v4f g = joined<2, T, KS>(red, t, lane), u = joined<2, T, KS>(red, T + t, lane);
+    const int j = j0 + t * 16 + r16;
+    if (j < n) {
+      float hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = silu_mul(g[i], u[i]);
+        hi[i] = (float)(__bf16)a;
+        // an infinity leaves no rest (and its difference would be NaN)
+        lo[i] = fabsf(hi[i]) <= 3.4028235e38f ? a - hi[i] : 0.0f;
+      }
+      uint8_t* at = c.act + ((size_t)list[j] * c.I + f * 16) * 4 + q4 * 8;
+      *reinterpret_cast<uint2*>(at) =
+          make_uint2(pack16x2<kBf16>(hi[0], hi[1]), pack16x2<kBf16>(hi[2], hi[3]));
+      *reinterpret_cast<uint2*>(at + 32) =
+          make_uint2(pack16x2<kBf16>(lo[0], lo[1]), pack16x2<kBf16>(lo[2], lo[3]));
+    }
+  }
+  __syncthreads();  // `red` is free
+}
+
+// Second product: workgroup (f, s) makes 16 * NB features of slot s's expert's
+// output for all its tokens, times their weights.
+template <int NB, int T, int KS>
+__device__ __forceinline__ void down_tokens(const MoeCall& c, int e, int j0, int n,
+                                            const uint16_t* list, v4f* red) {
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q4 = lane >> 4, r16 = lane & 15;
+  const int rb0 = blockIdx.x * NB, nrb = c.K / 16;
+  using P = Product<kBf16, NB, T, 2, KS>;
+  P p;
+  p.K = c.I;
+  p.KB = (c.I + kFp8Block - 1) / kFp8Block;
+  p.lane = lane;
+  p.q4 = q4;
+  p.w_bytes = (uint32_t)c.K * (uint32_t)(p.KB * kFp8Block);
+  p.W = c.down + (size_t)e * p.w_bytes;
+  const float* scales = c.down_scale + (size_t)e * ((c.K + 127) / 128) * p.KB;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int rb = min(rb0 + b, nrb - 1);  // past the end: the last one, never stored
+    p.w_at[b] = (uint32_t)rb * (uint32_t)p.KB * 2048u;
+    p.s_at[b] = (typename P::scalar_ptr)(uintptr_t)(scales + (size_t)(rb / 8) * p.KB);
+  }
+  p.X = c.act;
+  p.x_bytes = (uint32_t)c.M * (uint32_t)c.top_k * (uint32_t)c.I * 4u;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int j = j0 + t * 16 + r16;
+    p.rows[t] = j < n ? (uint32_t)list[j] * (uint32_t)c.I * 4u + q4 * 64u : kNoRow;
+  }
+  v4f acc[NB][T];
+  p.run(w, acc);
+  spread_partials<NB, T, KS>(acc, w, lane, red);
+  for (int o = w; o < NB * T; o += KS) {
+    const v4f y = joined<NB, T, KS>(red, o, lane);
+    const int j = j0 + o % T * 16 + r16, rb = rb0 + o / T;
+    if (j < n && rb < nrb) {
+      const float s = c.weights[list[j]];
+      *reinterpret_cast<v4f*>(c.part + (size_t)list[j] * c.K + rb * 16 + q4 * 4) = y * s;
+    }
+  }
+  __syncthreads();
+}
+
+template <int TY, int TMAX, int KS>
+__global__ __launch_bounds__(KS * 64) void k_moe_up(MoeCall c) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int counts[KS];
+  v4f* red = reinterpret_cast<v4f*>(smem);
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + KS * 2 * TMAX * 1024);
+  int n;
+  const int e = expert_of_slot<KS * 64>(c, blockIdx.y, list, counts, n);
+  if (e < 0) return;
+  for (int j0 = 0; j0 < n; j0 += 16 * TMAX) {
+    if (TMAX >= 4 && n - j0 > 32)
+      up_tokens<TY, TMAX, KS>(c, e, j0, n, list, red);
+    else if (TMAX >= 2 && n - j0 > 16)
+      up_tokens<TY, TMAX < 2 ? 1 : 2, KS>(c, e, j0, n, list, red);
+    else
+      up_tokens<TY, 1, KS>(c, e, j0, n, list, red);
+  }
+}
+
+template <int NB, int TMAX, int KS>
+__global__ __launch_bounds__(KS * 64) void k_moe_down(MoeCall c) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int counts[KS];
+  v4f* red = reinterpret_cast<v4f*>(smem);
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + KS * NB * TMAX * 1024);
+  int n;
+  const int e = expert_of_slot<KS * 64>(c, blockIdx.y, list, counts, n);
+  if (e < 0) return;
+  for (int j0 = 0; j0 < n; j0 += 16 * TMAX) {
+    if (TMAX >= 4 && n - j0 > 32)
+      down_tokens<NB, TMAX, KS>(c, e, j0, n, list, red);
+    else if (TMAX >= 2 && n - j0 > 16)
+      down_tokens<NB, TMAX < 2 ? 1 : 2, KS>(c, e, j0, n, list, red);
+    else
+      down_tokens<NB, 1, KS>(c, e, j0, n, list, red);
+  }
+}
+
+// y[m] = the sum of the token's pairs in their order, rounded once; a thread
+// per 8 columns.
+template <int TY>
+__global__ __launch_bounds__(256) void k_moe_join(MoeCall c) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int chunks = c.K / 8;
+  if (i >= (int64_t)c.M * chunks) return;
+  const int m = (int)(i / chunks), k = (int)(i % chunks) * 8;
+  v4f a = {}, b = {};
+  for (int j = 0; j < c.top_k; ++j) {
+    const int p = m * c.top_k + j;
+    if ((unsigned)c.experts[p] >= (unsigned)c.E) continue;  // its sums were not made
+    const v4f* from = reinterpret_cast<const v4f*>(c.part + (size_t)p * c.K + k);
+    a += from[0];
+    b += from[1];
+  }
+  *reinterpret_cast<uint4*>(c.Y + (size_t)m * c.K + k) =
+      make_uint4(pack16x2<TY>(a[0], a[1]), pack16x2<TY>(a[2], a[3]), pack16x2<TY>(b[0], b[1]),
+                 pack16x2<TY>(b[2], b[3]));
+}
+
+template <int TY, int TMAX>
+hipError_t run(const MoeCall& c, hipStream_t st) {
+  constexpr int KSU = TMAX == 1 ? 8 : 4, KSD = 4, NB = 2;
+  const int P = c.M * c.top_k, slots = P < c.E ? P : c.E;
+  const size_t list = (size_t)P * 2;
+  if (slots > 0) {
+    if (c.I > 0)
+      k_moe_up<TY, TMAX, KSU>
+          <<<dim3(c.I / 16, slots), KSU * 64, KSU * 2 * TMAX * 1024 + list, st>>>(c);
+    k_moe_down<NB, TMAX, KSD>
+        <<<dim3((c.K / 16 + NB - 1) / NB, slots), KSD * 64, KSD * NB * TMAX * 1024 + list, st>>>(c);
+  }
+  k_moe_join<TY><<<(unsigned)(((int64_t)c.M * (c.K / 8) + 255) / 256), 256, 0, st>>>(c);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_moe(const MoeCall& c, hipStream_t st) {
+  if (c.M <= 16) return c.type == kF16 ? run<kF16, 1>(c, st) : run<kBf16, 1>(c, st);
+  return c.type == kF16 ? run<kF16, 4>(c, st) : run<kBf16, 4>(c, st);
+}
+
+}  // namespace i8mm

@@ -24,7 +24,7 @@ import torch
 from . import _check, load
 
 __all__ = ["FP8_BLOCK", "fp8_kpad", "fp8_pack_weight", "fp8_quantize_weight", "fp8_quantize",
-           "fp8_rms_norm", "fp8_silu_mul", "fp8_matmul", "fp8_matmul_config"]
+           "fp8_rms_norm", "fp8_sandwich_norm", "fp8_silu_mul", "fp8_matmul", "fp8_matmul_config"]
 
 FP8_BLOCK = 128
 _E4M3 = torch.float8_e4m3fn
@@ -175,6 +175,52 @@ def fp8_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
                                float(eps), _at(H), _at(X_f8), _at(x_scale),
                                _stream_of(X.get_device())))
     return (X_f8, x_scale) if residual is None else (X_f8, x_scale, H)
+
+
+def fp8_sandwich_norm(X: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tensor,
+                      pre_weight: torch.Tensor, gate: torch.Tensor | None = None,
+                      residual_scale: float = 1.0, eps: float = 1e-6, quantize: bool = True,
+                      residual_out: torch.Tensor | None = None, out=None, stream=None):
+    """The norm after a block, the residual's addition and the norm before the
+    next block, for the block's output X and the stream `residual`, both [M,K]:
+        H = residual_scale * residual + gate * norm(X, post_weight)
+        Y = norm(H, pre_weight), of H before its rounding
+    gives (Y's e4m3, its scales, H), or with quantize=False (Y, H) in X's type.
+    `gate`: [G,K] with G dividing M, a row for M / G tokens after another, or
+    [K].  `residual_out` takes H and may be `residual` or X; `out` takes the
+    pair, or Y."""
+    _tensor(X, "X", _HALVES, 2)
+    if _elsewhere(X, stream):
+        outs = (out or ()) if quantize else (out,)
+        with _current(X, stream, residual, post_weight, pre_weight, gate, residual_out, *outs):
+            return fp8_sandwich_norm(X, residual, post_weight, pre_weight, gate, residual_scale, eps,
+                                     quantize, residual_out, out)
+    M, K = X.shape
+    dev, one = X.device, (X.dtype,)
+    _tensor(residual, "residual", one, (M, K), dev)
+    _tensor(post_weight, "post_weight", one, (K,), dev)
+    _tensor(pre_weight, "pre_weight", one, (K,), dev)
+    gates = 0
+    if gate is not None:
+        gates = 1 if gate.dim() == 1 else gate.shape[0]
+        _tensor(gate, "gate", one, (K,) if gate.dim() == 1 else (None, K), dev)
+        if gates == 0 or M % gates:
+            raise ValueError(f"gate has {gates} rows, which do not divide {M} tokens")
+    H = residual_out
+    if H is None:
+        H = torch.empty_like(X)
+    else:
+        _tensor(H, "residual_out", one, (M, K), dev)
+    Y = X_f8 = x_scale = None
+    if quantize:
+        X_f8, x_scale = _quantized(out, M, K, dev, X)
+    else:
+        Y = torch.empty_like(X) if out is None else _tensor(out, "out", one, (M, K), dev)
+    _check(load().fp8_sandwich_norm(_at(X), _at(residual), _at(post_weight), _at(pre_weight),
+                                    _at(gate), gates if K else 0, float(residual_scale), _TYPES[X.dtype],
+                                    M, K, float(eps), _at(H), _at(Y), _at(X_f8), _at(x_scale),
+                                    _stream_of(X.get_device())))
+    return (X_f8, x_scale, H) if quantize else (Y, H)
 
 
 def fp8_silu_mul(gate_up: torch.Tensor, out=None, stream=None):
