@@ -17,6 +17,9 @@
 #include "launch.hpp"
 #include "moe.hpp"
 
+#include <atomic>
+#include <type_traits>
+
 namespace i8mm {
 
 namespace {
@@ -214,6 +217,22 @@ __device__ __forceinline__ v4f joined(const v4f* red, int o, int lane) {
   return y;
 }
 
+// The gated product of a lane's four features of one pair, as two bf16 numbers.
+__device__ __forceinline__ void store_gated(const v4f& g, const v4f& u, uint8_t* at) {
+  float hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = silu_mul(g[i], u[i]);
+    hi[i] = (float)(__bf16)a;
+    // an infinity leaves no rest (and its difference would be NaN)
+    lo[i] = fabsf(hi[i]) <= 3.4028235e38f ? a - hi[i] : 0.0f;
+  }
+  *reinterpret_cast<uint2*>(at) =
+      make_uint2(pack16x2<kBf16>(hi[0], hi[1]), pack16x2<kBf16>(hi[2], hi[3]));
+  *reinterpret_cast<uint2*>(at + 32) =
+      make_uint2(pack16x2<kBf16>(lo[0], lo[1]), pack16x2<kBf16>(lo[2], lo[3]));
+}
+
 // First product: workgroup (f, s) makes 16 features of the gated product, gate
 // and up rows side by side, for all tokens of slot s's expert.
 template <int TY, int T, int KS>
@@ -252,19 +271,7 @@ __device__ __forceinline__ void up_tokens(const MoeCall& c, int e, int j0, int n
     const v4f g = joined<2, T, KS>(red, t, lane), u = joined<2, T, KS>(red, T + t, lane);
     const int j = j0 + t * 16 + r16;
     if (j < n) {
-      float hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = silu_mul(g[i], u[i]);
-        hi[i] = (float)(__bf16)a;
-        // an infinity leaves no rest (and its difference would be NaN)
-        lo[i] = fabsf(hi[i]) <= 3.4028235e38f ? a - hi[i] : 0.0f;
-      }
-      uint8_t* at = c.act + ((size_t)list[j] * c.I + f * 16) * 4 + q4 * 8;
-      *reinterpret_cast<uint2*>(at) =
-          make_uint2(pack16x2<kBf16>(hi[0], hi[1]), pack16x2<kBf16>(hi[2], hi[3]));
-      *reinterpret_cast<uint2*>(at + 32) =
-          make_uint2(pack16x2<kBf16>(lo[0], lo[1]), pack16x2<kBf16>(lo[2], lo[3]));
+      store_gated(g, u, c.act + ((size_t)list[j] * c.I + f * 16) * 4 + q4 * 8);
     }
   }
   __syncthreads();  // `red` is free
@@ -353,6 +360,235 @@ __global__ __launch_bounds__(KS * 64) void k_moe_down(MoeCall c) {
   }
 }
 
+// ---- many workgroups: no split of the columns --------------------------------
+//
+// A workgroup's eight wavefronts take two blocks of 16 weight rows each, over all
+// columns, and share the tokens' tile of a 128-column block in LDS (two stages;
+// the next one travels through registers under the products of this one).  The
+// weights go straight to the wavefront that uses them, up to two blocks ahead.
+// A tile row is 256 bytes per number of an operand column, its 16-byte chunks
+// swapped by the row's low three bits so that eight rows' reads of one chunk
+// meet all banks.
+template <int TY, int T, int PLANES>
+struct Wide {
+  static constexpr int WAVES = 8, NB = 2, NT = WAVES * 64;
+  static constexpr int ROW = 256 * PLANES, CHUNKS = ROW / 16;
+  static constexpr int STAGE = T * 16 * ROW;
+  static constexpr int LOADS = (T * 16 * CHUNKS + NT - 1) / NT;
+  typedef const __attribute__((address_space(4))) float* scalar_ptr;
+  struct Weights {
+    v4i w[NB][2];
+    float s[NB];
+  };
+  const uint8_t* W;
+  uint32_t w_bytes;
+  uint32_t w_at[NB];
+  scalar_ptr s_at[NB];
+  const void* X;
+  uint32_t x_bytes;
+  int K, KB;
+
+  // list[j0 .. j0 + 16 T) of n pairs are the tile's rows; a row's operand starts
+  // at byte (pair / per) * stride.
+  __device__ __forceinline__ void run(const uint16_t* list, int j0, int n, int per, uint32_t stride,
+                                      uint8_t* smem, v4f (&acc)[NB][T]) const {
+    const int tid = threadIdx.x, lane = tid & 63, q4 = lane >> 4, r16 = lane & 15;
+    const __amdgpu_buffer_rsrc_t rw =
+        __builtin_amdgcn_make_buffer_rsrc((void*)W, (short)0, (int)w_bytes, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rx =
+        __builtin_amdgcn_make_buffer_rsrc((void*)X, (short)0, (int)x_bytes, 0x00020000);
+    // The tile's chunk number i * NT + thread of LDS holds the swapped chunk of its row.
+    uint32_t src[LOADS];
+    const int slot = tid % CHUNKS, row0 = tid / CHUNKS;
+    const int c = slot ^ (row0 & 7);  // NT / CHUNKS rows further the low bits are the same
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int j = j0 + row0 + i * (NT / CHUNKS);
+      src[i] = j < n ? (uint32_t)(list[j] / per) * stride + c * 16u : kNoRow;
+    }
+    // columns of a chunk: 8 of one number, or 16 of two numbers in four chunks
+    const int col = PLANES == 1 ? c * 8 : (c >> 2) * 16;
+    const int first = __builtin_amdgcn_readfirstlane(tid & ~63);
+    auto load_x = [&](int kb, int stage) {
+      const bool out = kb * 128 + col >= K;
+      uint8_t* dst = smem + stage * STAGE + first * 16;
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        if (i * NT + first < T * 16 * CHUNKS)  // whole wavefronts
+          dma16(rx, dst + i * NT * 16, (int)(out ? kNoRow : src[i]), kb * ROW);
+    };
+    auto load_w = [&](int kb, Weights& o) {
+      constexpr int kNonTemporal = 2;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        o.s[b] = s_at[b][kb];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          o.w[b][h] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                       rw, lane * 16, (int)(w_at[b] + (uint32_t)kb * 2048u + h * 1024u),
+                       kNonTemporal));
+      }
+    };
+    auto compute = [&](const Weights& o, int stage) {
+      v4i w[2][NB][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) widen16<TY>(o.w[b][h], w[h][b]);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const uint8_t* row = smem + stage * STAGE + (t * 16 + r16) * ROW;
+        v4f sum[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) sum[b] = v4f{};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int c = (h * 4 + q4) * 2 * PLANES + p * 2 + i;
+              const v4i f = *reinterpret_cast<const v4i*>(row + (c ^ (r16 & 7)) * 16);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) sum[b] = mfma32<TY>(w[h][b][i], f, sum[b]);
+            }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[b][t][e] = fmaf(sum[b][e], o.s[b], acc[b][t][e]);
+        // one block of tokens' reads at a time: more would not fit the registers
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int t = 0; t < T; ++t) acc[b][t] = v4f{};
+    if (KB == 0) return;
+    Weights a, b;
+    load_x(0, 0);
+    load_w(0, a);
+    load_w(min(1, KB - 1), b);
+    constexpr int WOPS = 2 * NB;  // vector loads of a block's weights
+    barrier_vm<2 * WOPS>();       // the tile is there
+    auto step = [&](int kb, Weights& cur) {
+      const int stage = kb & 1;
+      load_x(min(kb + 1, KB - 1), stage ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(cur, stage);
+      load_w(min(kb + 2, KB - 1), cur);
+      // the next tile is there, and this one free
+      barrier_vm<WOPS>();
+    };
+    for (int kb = 0; kb < KB; kb += 2) {
+      step(kb, a);
+      if (kb + 1 < KB) step(kb + 1, b);
+    }
+    barrier_vm<0>();  // no DMA may still write LDS
+  }
+};
+
+template <int TY, int T>
+__device__ __forceinline__ void up_wide(const MoeCall& c, int e, int j0, int n,
+                                        const uint16_t* list, uint8_t* smem) {
+  const int lane = threadIdx.x & 63, q4 = lane >> 4, r16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  using P = Wide<TY, T, 1>;
+  const int f = blockIdx.x * P::WAVES + w, nf = c.I / 16, fc = min(f, nf - 1);
+  P p;
+  p.K = c.K;
+  p.KB = (c.K + kFp8Block - 1) / kFp8Block;
+  p.w_bytes = (uint32_t)(2 * c.I) * (uint32_t)(p.KB * kFp8Block);
+  p.W = c.up + (size_t)e * p.w_bytes;
+  const float* scales = c.up_scale + (size_t)e * ((2 * c.I + 127) / 128) * p.KB;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int rb = b * nf + fc;
+    p.w_at[b] = (uint32_t)rb * (uint32_t)p.KB * 2048u;
+    p.s_at[b] = (typename P::scalar_ptr)(uintptr_t)(scales + (size_t)(rb / 8) * p.KB);
+  }
+  p.X = c.X;
+  p.x_bytes = (uint32_t)c.M * (uint32_t)c.K * 2u;
+  v4f acc[2][T];
+  p.run(list, j0, n, c.top_k, (uint32_t)c.K * 2u, smem, acc);
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int j = j0 + t * 16 + r16;
+    if (j < n && f < nf)
+      store_gated(acc[0][t], acc[1][t], c.act + ((size_t)list[j] * c.I + f * 16) * 4 + q4 * 8);
+  }
+}
+
+template <int T>
+__device__ __forceinline__ void down_wide(const MoeCall& c, int e, int j0, int n,
+                                          const uint16_t* list, uint8_t* smem) {
+  const int lane = threadIdx.x & 63, q4 = lane >> 4, r16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  using P = Wide<kBf16, T, 2>;
+  const int rb0 = (blockIdx.x * P::WAVES + w) * 2, nrb = c.K / 16;
+  P p;
+  p.K = c.I;
+  p.KB = (c.I + kFp8Block - 1) / kFp8Block;
+  p.w_bytes = (uint32_t)c.K * (uint32_t)(p.KB * kFp8Block);
+  p.W = c.down + (size_t)e * p.w_bytes;
+  const float* scales = c.down_scale + (size_t)e * ((c.K + 127) / 128) * p.KB;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int rb = min(rb0 + b, nrb - 1);
+    p.w_at[b] = (uint32_t)rb * (uint32_t)p.KB * 2048u;
+    p.s_at[b] = (typename P::scalar_ptr)(uintptr_t)(scales + (size_t)(rb / 8) * p.KB);
+  }
+  p.X = c.act;
+  p.x_bytes = (uint32_t)c.M * (uint32_t)c.top_k * (uint32_t)c.I * 4u;
+  v4f acc[2][T];
+  p.run(list, j0, n, 1, (uint32_t)c.I * 4u, smem, acc);
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int j = j0 + t * 16 + r16;
+    if (j < n) {
+      const float s = c.weights[list[j]];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (rb0 + b < nrb)
+          *reinterpret_cast<v4f*>(c.part + (size_t)list[j] * c.K + (rb0 + b) * 16 + q4 * 4) =
+              acc[b][t] * s;
+    }
+  }
+}
+
+// UP: the first product, else the second.  Up to 16 * TMAX of an expert's tokens
+// per pass over its weights.
+template <int TY, bool UP, int TMAX>
+__global__ __launch_bounds__(512, TMAX == 1 ? 6 : 4) void k_moe_wide(MoeCall c) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int counts[8];
+  constexpr int TILE = 2 * Wide<TY, TMAX, UP ? 1 : 2>::STAGE;
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + TILE);
+  int n;
+  const int e = expert_of_slot<512>(c, blockIdx.y, list, counts, n);
+  if (e < 0) return;
+  auto pass = [&](auto t, int j0) {
+    if constexpr (t() <= TMAX) {
+      if constexpr (UP)
+        up_wide<TY, t()>(c, e, j0, n, list, smem);
+      else
+        down_wide<t()>(c, e, j0, n, list, smem);
+    }
+  };
+  for (int j0 = 0; j0 < n; j0 += 16 * TMAX) {
+    const int blocks = min((n - j0 + 15) / 16, TMAX);
+    if (blocks == 4)
+      pass(std::integral_constant<int, 4>{}, j0);
+    else if (blocks == 3)
+      pass(std::integral_constant<int, 3>{}, j0);
+    else if (blocks == 2)
+      pass(std::integral_constant<int, 2>{}, j0);
+    else
+      pass(std::integral_constant<int, 1>{}, j0);
+  }
+}
+
 // y[m] = the sum of the token's pairs in their order, rounded once; a thread
 // per 8 columns.
 template <int TY>
@@ -374,18 +610,55 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeCall c) {
                  pack16x2<TY>(b[2], b[3]));
 }
 
-template <int TY, int TMAX>
-hipError_t run(const MoeCall& c, hipStream_t st) {
-  constexpr int KSU = TMAX == 1 ? 8 : 4, KSD = 4, NB = 2;
-  const int P = c.M * c.top_k, slots = P < c.E ? P : c.E;
-  const size_t list = (size_t)P * 2;
-  if (slots > 0) {
-    if (c.I > 0)
-      k_moe_up<TY, TMAX, KSU>
-          <<<dim3(c.I / 16, slots), KSU * 64, KSU * 2 * TMAX * 1024 + list, st>>>(c);
-    k_moe_down<NB, TMAX, KSD>
-        <<<dim3((c.K / 16 + NB - 1) / NB, slots), KSD * 64, KSD * NB * TMAX * 1024 + list, st>>>(c);
+// Launches with more than the 64 KB of dynamic LDS that need no leave: asked
+// for once per device the kernels run on.
+template <typename Kernel>
+hipError_t launch_big(Kernel kern, std::atomic<uint64_t>& asked, dim3 grid, int threads, size_t lds,
+                      const MoeCall& c, hipStream_t st) {
+  int dev = 0;
+  (void)hipGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(asked.load(std::memory_order_relaxed) & bit)) {
+    const hipError_t e = hipFuncSetAttribute(
+        (const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    if (e != hipSuccess) return e;
+    asked.fetch_or(bit, std::memory_order_relaxed);
   }
+  kern<<<grid, threads, lds, st>>>(c);
+  return hipGetLastError();
+}
+
+template <int TY, int TMAX>
+hipError_t run_split(const MoeCall& c, int slots, hipStream_t st) {
+  constexpr int KSU = TMAX == 1 ? 8 : 4, KSD = 4, NB = 2;
+  const size_t list = (size_t)c.M * c.top_k * 2;
+  if (c.I > 0)
+    k_moe_up<TY, TMAX, KSU><<<dim3(c.I / 16, slots), KSU * 64, KSU * 2 * TMAX * 1024 + list, st>>>(c);
+  k_moe_down<NB, TMAX, KSD>
+      <<<dim3((c.K / 16 + NB - 1) / NB, slots), KSD * 64, KSD * NB * TMAX * 1024 + list, st>>>(c);
+  return hipGetLastError();
+}
+
+template <int TY, int TMAX>
+hipError_t run_wide(const MoeCall& c, int slots, hipStream_t st) {
+  static std::atomic<uint64_t> asked[2];
+  const size_t list = (size_t)c.M * c.top_k * 2;
+  hipError_t e = launch_big(k_moe_wide<TY, true, TMAX>, asked[0], dim3((c.I / 16 + 7) / 8, slots),
+                            512, 2 * Wide<TY, TMAX, 1>::STAGE + list, c, st);
+  if (e != hipSuccess) return e;
+  return launch_big(k_moe_wide<kBf16, false, TMAX>, asked[1], dim3((c.K / 16 + 15) / 16, slots),
+                    512, 2 * Wide<TY, TMAX, 2>::STAGE + list, c, st);
+}
+
+template <int TY>
+hipError_t run(const MoeCall& c, hipStream_t st) {
+  const int P = c.M * c.top_k, slots = P < c.E ? P : c.E;
+  hipError_t e;
+  if (c.M > 16 && c.I > 0)
+    e = run_wide<TY, 4>(c, slots, st);
+  else
+    e = c.M <= 16 ? run_split<TY, 1>(c, slots, st) : run_split<TY, 4>(c, slots, st);
+  if (e != hipSuccess) return e;
   k_moe_join<TY><<<(unsigned)(((int64_t)c.M * (c.K / 8) + 255) / 256), 256, 0, st>>>(c);
   return hipGetLastError();
 }
@@ -393,8 +666,7 @@ hipError_t run(const MoeCall& c, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_fp8_moe(const MoeCall& c, hipStream_t st) {
-  if (c.M <= 16) return c.type == kF16 ? run<kF16, 1>(c, st) : run<kBf16, 1>(c, st);
-  return c.type == kF16 ? run<kF16, 4>(c, st) : run<kBf16, 4>(c, st);
+  return c.type == kF16 ? run<kF16>(c, st) : run<kBf16>(c, st);
 }
 
 }  // namespace i8mm
