@@ -120,14 +120,12 @@ struct Product {
   uint32_t rows[T];
   int K, KB, lane, q4;
 
-  __device__ __forceinline__ void load(int kb, Stage& o) const {
+  __device__ __forceinline__ void load_w(int kb, Stage& o) const {
     constexpr int kNonTemporal = 2;
     const bool live = kb < KB;
     const int k = live ? kb : 0;
     const __amdgpu_buffer_rsrc_t rw =
         __builtin_amdgcn_make_buffer_rsrc((void*)W, (short)0, live ? (int)w_bytes : 0, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rx =
-        __builtin_amdgcn_make_buffer_rsrc((void*)X, (short)0, live ? (int)x_bytes : 0, 0x00020000);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       o.s[b] = s_at[b][k];
@@ -137,6 +135,13 @@ struct Product {
             v4i, __builtin_amdgcn_raw_buffer_load_b128(
                      rw, lane * 16, (int)(w_at[b] + (uint32_t)k * 2048u + h * 1024u), kNonTemporal));
     }
+  }
+
+  __device__ __forceinline__ void load_x(int kb, Stage& o) const {
+    const bool live = kb < KB;
+    const int k = live ? kb : 0;
+    const __amdgpu_buffer_rsrc_t rx =
+        __builtin_amdgcn_make_buffer_rsrc((void*)X, (short)0, live ? (int)x_bytes : 0, 0x00020000);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const bool out = k * 128 + h * 64 + q4 * 16 >= K;
@@ -188,12 +193,15 @@ struct Product {
       for (int t = 0; t < T; ++t) acc[b][t] = v4f{};
     if (w >= KB) return;
     Stage a, b;
-    load(w, a);
+    load_x(w, a);
+    load_w(w, a);
     for (int kb = w; kb < KB; kb += 2 * KS) {
-      load(kb + KS, b);
+      load_x(kb + KS, b);
+      load_w(kb + KS, b);
       compute(a, acc);
       if (kb + KS >= KB) break;
-      load(kb + 2 * KS, a);
+      load_x(kb + 2 * KS, a);
+      load_w(kb + 2 * KS, a);
       compute(b, acc);
     }
   }
@@ -589,8 +597,232 @@ __global__ __launch_bounds__(512, TMAX == 1 ? 6 : 4) void k_moe_wide(MoeCall c) 
   }
 }
 
+// ---- a few pairs: vector products -------------------------------------------
+//
+// With far fewer pairs than experts an expert has hardly ever two tokens, so each
+// pair goes alone, without matrix instructions: a lane multiplies its 16 numbers
+// of a row by the pair's activations (fp32, in LDS, read by 16 lanes at once).
+// That needs one accumulator and no operand registers, so CB blocks of weights
+// are on their way at once; what these calls wait for is latency.
+
+// The sums over columns [kb0, kb1) * 128 of NB row blocks; lane l has that of row
+// l % 16 in every of its four quarters.  x.load(kb) starts the loads of the
+// activations of CB blocks (zeros past the end) and x.store(at) leaves them as
+// fp32 in LDS of the wavefront's own.  Those of kb0 are on their way already:
+// they do not wait for what the weights' address waits for.
+template <int NB, int CB, typename Activations>
+__device__ __forceinline__ void vector_product(const uint8_t* W, uint32_t w_bytes,
+                                               const uint32_t (&w_at)[NB],
+                                               const float* const (&s_at)[NB], int kb0, int kb1,
+                                               float* at, Activations& x, float (&acc)[NB]) {
+  constexpr int kNonTemporal = 2;
+  const int lane = threadIdx.x & 63, q4 = lane >> 4;
+  v4i w[CB][NB][2];
+  float s[NB];
+  // a block at or past kb1 gets an empty descriptor: zeros, and nothing is read
+  auto load_w = [&](int kb, v4i (&o)[NB][2]) {
+    const bool live = kb < kb1;
+    const __amdgpu_buffer_rsrc_t rw =
+        __builtin_amdgcn_make_buffer_rsrc((void*)W, (short)0, live ? (int)w_bytes : 0, 0x00020000);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        o[b][h] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                     rw, lane * 16 + h * 1024, live ? (int)(w_at[b] + (uint32_t)kb * 2048u) : 0,
+                     kNonTemporal));
+  };
+  // the blocks' scales, one a lane: scalar loads would be waited for with the
+  // first read of LDS
+  auto load_scales = [&](int kb) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) s[b] = s_at[b][min(kb + lane, kb1 - 1)];
+  };
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = 0.0f;
+  if (kb0 >= kb1) return;
+  load_scales(kb0);
+#pragma unroll
+  for (int c = 0; c < CB; ++c) load_w(kb0 + c, w[c]);
+  for (int kb = kb0; kb < kb1; kb += CB) {
+    x.store(at);
+    float now[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) now[b] = s[b];
+    if (kb + CB < kb1) {
+      x.load(kb + CB);
+      load_scales(kb + CB);
+    }
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+      float sum[NB][2] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v4f* from = reinterpret_cast<const v4f*>(at + c * 128 + h * 64 + q4 * 16);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const v4f v = from[d];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            typedef float v2f __attribute__((ext_vector_type(2)));
+            const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[c][b][h][d], false);
+            const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[c][b][h][d], true);
+            sum[b][0] = fmaf(lo[0], v[0], sum[b][0]);
+            sum[b][1] = fmaf(lo[1], v[1], sum[b][1]);
+            sum[b][0] = fmaf(hi[0], v[2], sum[b][0]);
+            sum[b][1] = fmaf(hi[1], v[3], sum[b][1]);
+          }
+          // else the reads and conversions of all blocks are brought forward, and
+          // their registers cost more than they hide
+          if (d & 1) __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      load_w(kb + CB + c, w[c]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float sc = __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, now[b]), c));
+        acc[b] = fmaf(sum[b][0] + sum[b][1], sc, acc[b]);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before it is written again
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    acc[b] += __shfl_xor(acc[b], 16, kWave);
+    acc[b] += __shfl_xor(acc[b], 32, kWave);
+  }
+}
+
+// First product: workgroup (f, p) makes 16 features of pair p's gated product
+// (fp32), the columns split over its wavefronts.
+constexpr int kFewUpWaves = 8, kFewUpBlocks = 2;
+template <int TY>
+struct FewTokens {
+  const uint16_t* row;
+  int K, lane;
+  uint2 v;
+  __device__ __forceinline__ void load(int kb) {  // 4 columns a lane
+    static_assert(kFewUpBlocks * 128 == 64 * 4, "one load per lane");
+    const int k = kb * 128 + lane * 4;
+    v = k < K ? *reinterpret_cast<const uint2*>(row + k) : make_uint2(0, 0);
+  }
+  __device__ __forceinline__ void store(float* at) const {
+    *reinterpret_cast<v4f*>(at + lane * 4) =
+        v4f{to_f32<TY>((uint16_t)v.x), to_f32<TY>((uint16_t)(v.x >> 16)),
+            to_f32<TY>((uint16_t)v.y), to_f32<TY>((uint16_t)(v.y >> 16))};
+  }
+};
+template <int TY>
+__global__ __launch_bounds__(kFewUpWaves * 64) void k_moe_up_few(MoeCall c) {
+  __shared__ __align__(16) float x[kFewUpWaves][kFewUpBlocks * 128];
+  __shared__ float red[kFewUpWaves][2][16];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int f = blockIdx.x, pair = blockIdx.y;
+  const int KB = (c.K + kFp8Block - 1) / kFp8Block;
+  const int kb0 = KB * w / kFewUpWaves, kb1 = KB * (w + 1) / kFewUpWaves;
+  // columns past the wavefront's own meet weights of zero, and are none themselves
+  FewTokens<TY> tokens{c.X + (size_t)(pair / c.top_k) * c.K, min(c.K, kb1 * 128), lane, {}};
+  tokens.load(kb0);
+  const int e = __builtin_amdgcn_readfirstlane(c.experts[pair]);
+  if ((unsigned)e >= (unsigned)c.E) return;
+  const uint32_t w_bytes = (uint32_t)(2 * c.I) * (uint32_t)(KB * kFp8Block);
+  uint32_t w_at[2];
+  const float* s_at[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int rb = b * (c.I / 16) + f;
+    w_at[b] = (uint32_t)rb * (uint32_t)KB * 2048u;
+    s_at[b] = c.up_scale + ((size_t)e * ((2 * c.I + 127) / 128) + rb / 8) * KB;
+  }
+  float acc[2];
+  vector_product<2, kFewUpBlocks>(c.up + (size_t)e * w_bytes, w_bytes, w_at, s_at, kb0, kb1, x[w],
+                                  tokens, acc);
+  if (lane < 16) red[w][0][lane] = acc[0], red[w][1][lane] = acc[1];
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kFewUpWaves; ++i) g += red[i][0][lane], u += red[i][1][lane];
+    reinterpret_cast<float*>(c.act)[(size_t)pair * c.I + f * 16 + lane] = silu_mul(g, u);
+  }
+}
+
+// Second product and the sum over the pairs: a workgroup owns 16 features of all
+// pairs; its wavefronts take the pairs in turn, or, where there are fewer pairs,
+// one of `parts` shares of a pair's columns.
+constexpr int kFewDownWaves = 16, kFewDownBlocks = 2;
+constexpr int kFewPairs = 64;
+struct FewGated {
+  const float* row;
+  int I, lane;
+  v4f v[kFewDownBlocks / 2];
+  __device__ __forceinline__ void load(int kb) {  // 4 columns a lane and load
+#pragma unroll
+    for (int i = 0; i < kFewDownBlocks / 2; ++i) {
+      const int k = kb * 128 + i * 256 + lane * 4;
+      v[i] = k < I ? *reinterpret_cast<const v4f*>(row + k) : v4f{};
+    }
+  }
+  __device__ __forceinline__ void store(float* at) const {
+#pragma unroll
+    for (int i = 0; i < kFewDownBlocks / 2; ++i)
+      *reinterpret_cast<v4f*>(at + i * 256 + lane * 4) = v[i];
+  }
+};
+template <int TY>
+__global__ __launch_bounds__(kFewDownWaves * 64) void k_moe_down_few(MoeCall c, int parts) {
+  __shared__ __align__(16) float x[kFewDownWaves][kFewDownBlocks * 128];
+  __shared__ float sums[kFewPairs][16];  // parts * pairs <= kFewPairs
+  __shared__ float shares[kFewPairs];    // the pairs' weights
+  const int P = c.M * c.top_k;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rb = blockIdx.x, KB = (c.I + kFp8Block - 1) / kFp8Block;
+  const uint32_t w_bytes = (uint32_t)c.K * (uint32_t)(KB * kFp8Block);
+  const uint32_t w_at[1] = {(uint32_t)rb * (uint32_t)KB * 2048u};
+  // a pair without an expert: zeros, whatever its weight
+  float share = 0.0f;
+  if (tid < P && (unsigned)c.experts[tid] < (unsigned)c.E) share = c.weights[tid];
+  for (int item = w; item < P * parts; item += kFewDownWaves) {
+    const int pair = item / parts, q = item % parts;
+    const int kb0 = KB * q / parts, kb1 = KB * (q + 1) / parts;
+    FewGated gated{reinterpret_cast<const float*>(c.act) + (size_t)pair * c.I,
+                   min(c.I, kb1 * 128), lane, {}};
+    gated.load(kb0);
+    const int e = __builtin_amdgcn_readfirstlane(c.experts[pair]);
+    if ((unsigned)e >= (unsigned)c.E) {
+      if (lane < 16) sums[item][lane] = 0.0f;
+      continue;
+    }
+    const float* const s_at[1] = {c.down_scale + ((size_t)e * ((c.K + 127) / 128) + rb / 8) * KB};
+    float acc[1];
+    vector_product<1, kFewDownBlocks>(c.down + (size_t)e * w_bytes, w_bytes, w_at, s_at, kb0, kb1,
+                                      x[w], gated, acc);
+    if (lane < 16) sums[item][lane] = acc[0];
+  }
+  if (tid < P) shares[tid] = share;
+  __syncthreads();
+  for (int o = tid; o < c.M * 16; o += kFewDownWaves * 64) {
+    const int m = o >> 4, f = o & 15;
+    float y = 0.0f;
+    for (int j = 0; j < c.top_k; ++j) {
+      const int pair = m * c.top_k + j;
+      float v = 0.0f;
+      for (int q = 0; q < parts; ++q) v += sums[pair * parts + q][f];
+      y = fmaf(v, shares[pair], y);
+    }
+    c.Y[(size_t)m * c.K + rb * 16 + f] = (uint16_t)pack16x2<TY>(y, 0.0f);
+  }
+}
+
 // y[m] = the sum of the token's pairs in their order, rounded once; a thread
-// per 8 columns.
+// per 8 columns.  Eight pairs' loads at a time, also those of pairs whose sums
+// were not made (their places are read and dropped): with a branch around each
+// load one token of 8 experts took 4.8 us instead of 2.
 template <int TY>
 __global__ __launch_bounds__(256) void k_moe_join(MoeCall c) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -598,12 +830,24 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeCall c) {
   if (i >= (int64_t)c.M * chunks) return;
   const int m = (int)(i / chunks), k = (int)(i % chunks) * 8;
   v4f a = {}, b = {};
-  for (int j = 0; j < c.top_k; ++j) {
-    const int p = m * c.top_k + j;
-    if ((unsigned)c.experts[p] >= (unsigned)c.E) continue;  // its sums were not made
-    const v4f* from = reinterpret_cast<const v4f*>(c.part + (size_t)p * c.K + k);
-    a += from[0];
-    b += from[1];
+  for (int j0 = 0; j0 < c.top_k; j0 += 8) {
+    v4f u[8], v[8];
+    bool made[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int p = m * c.top_k + min(j0 + j, c.top_k - 1);
+      made[j] = j0 + j < c.top_k && (unsigned)c.experts[p] < (unsigned)c.E;
+      const v4f* from = reinterpret_cast<const v4f*>(c.part + (size_t)p * c.K + k);
+      u[j] = from[0];
+      v[j] = from[1];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] += made[j] ? u[j][e] : 0.0f;
+        b[e] += made[j] ? v[j][e] : 0.0f;
+      }
   }
   *reinterpret_cast<uint4*>(c.Y + (size_t)m * c.K + k) =
       make_uint4(pack16x2<TY>(a[0], a[1]), pack16x2<TY>(a[2], a[3]), pack16x2<TY>(b[0], b[1]),
@@ -650,14 +894,37 @@ hipError_t run_wide(const MoeCall& c, int slots, hipStream_t st) {
                     512, 2 * Wide<TY, TMAX, 2>::STAGE + list, c, st);
 }
 
+// Whether each pair goes alone: one token, or so few pairs that they seldom
+// share an expert, whose weights are then read for each of them (us with and
+// without, tokens x columns, expert's width, experts, places: 1x4096 1408 128 8
+// 29.5 and 35.7; 2x4096 1408 128 8 53.0 and 61.7; 4x4096 1408 128 8 90.2 and 99.1;
+// 8x4096 1408 128 8 168 and 149; 1x5120 8192 8 2 52.9 and 59.5; 2x5120 8192 8 2
+// 86.8 and 87.1; 2x2048 768 128 8 22.7 and 27.4).
+bool few_pairs(const MoeCall& c) {
+  const int P = c.M * c.top_k;
+  return P <= kFewPairs && (c.M == 1 || 4 * P <= c.E);
+}
+
+template <int TY>
+hipError_t run_few(const MoeCall& c, hipStream_t st) {
+  const int P = c.M * c.top_k;
+  if (c.I > 0) k_moe_up_few<TY><<<dim3(c.I / 16, P), kFewUpWaves * 64, 0, st>>>(c);
+  const int parts = P < kFewDownWaves ? kFewDownWaves / P : 1;
+  k_moe_down_few<TY><<<c.K / 16, kFewDownWaves * 64, 0, st>>>(c, parts);
+  return hipGetLastError();
+}
+
 template <int TY>
 hipError_t run(const MoeCall& c, hipStream_t st) {
   const int P = c.M * c.top_k, slots = P < c.E ? P : c.E;
-  hipError_t e;
-  if (c.M > 16 && c.I > 0)
-    e = run_wide<TY, 4>(c, slots, st);
-  else
-    e = c.M <= 16 ? run_split<TY, 1>(c, slots, st) : run_split<TY, 4>(c, slots, st);
+  if (few_pairs(c)) return run_few<TY>(c, st);
+  hipError_t e = hipSuccess;
+  if (slots > 0) {
+    if (c.M <= 16)
+      e = run_split<TY, 1>(c, slots, st);
+    else
+      e = c.I > 0 ? run_wide<TY, 4>(c, slots, st) : run_split<TY, 4>(c, slots, st);
+  }
   if (e != hipSuccess) return e;
   k_moe_join<TY><<<(unsigned)(((int64_t)c.M * (c.K / 8) + 255) / 256), 256, 0, st>>>(c);
   return hipGetLastError();
