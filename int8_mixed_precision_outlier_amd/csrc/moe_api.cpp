@@ -41,7 +41,8 @@ int check_moe(int64_t M, int64_t K, int64_t I, int64_t E, int64_t top_k) {
 extern "C" {
 
 size_t moe_route_workspace_size(int64_t M, int64_t K, int64_t E, int64_t top_k) {
-  return check_route(M, K, E, top_k) == INT8MM_OK ? moe_align((size_t)M * E * sizeof(double)) : 0;
+  if (check_route(M, K, E, top_k) != INT8MM_OK) return 0;
+  return moe_align(route_logits_bytes(M, E)) + moe_align(route_bound_bytes(M, K, E));
 }
 
 int moe_route(const void* X, const void* W, int type, int64_t M, int64_t K, int64_t E,
@@ -57,8 +58,10 @@ int moe_route(const void* X, const void* W, int type, int64_t M, int64_t K, int6
     return INT8MM_EALIGN;
   if (workspace_bytes < moe_route_workspace_size(M, K, E, top_k)) return INT8MM_EWORKSPACE;
   const RouteCall c{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), experts,
-                    weights, static_cast<double*>(workspace), (int)M, (int)K, (int)E, (int)top_k,
-                    type, normalize != 0};
+                    weights, static_cast<double*>(workspace),
+                    reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                             moe_align(route_logits_bytes(M, E))),
+                    (int)M, (int)K, (int)E, (int)top_k, type, normalize != 0};
   return hip_error_status(launch_moe_route(c, stream));
 }
 

@@ -18,7 +18,12 @@ Tolerances, derived:
            rounded to fp32, is off by 2^-24 of itself, and so is its
            exponential by that times |difference|; expf 2 half steps (1 ulp),
            the sum of up to 1024 terms 16 + 6 additions, two divisions, the sum
-           over the chosen ones 32: (64 + |l - max|) * 2^-24.
+           over the chosen ones 32: (64 + |l - max|) * 2^-24.  Above 2^25 products
+           (tokens x columns x experts) a logit is a 64-bit sum of fp32 sums of 32
+           exact products: 31 additions each within 2^-23 of the running
+           magnitude, so it is off by b = 32 * 2^-23 sum |x w| at most, and a
+           weight by the factor exp(2 b) of the largest b of its token: its own
+           exponential's and the sum's.
   experts  a block of 128 columns: 4 instructions of 32 exact products, each of
            whose additions is within 2^-23 of the running magnitude, then one fma
            per block and at most 8 partial sums: (128 + KB + 8) * 2^-23 of the
@@ -150,7 +155,10 @@ def test_sandwich_norm_buffers(dtype):
 # ---- router ------------------------------------------------------------------
 
 ROUTES = [(1, 16, 1, 1), (1, 4096, 128, 8), (3, 144, 2, 2), (5, 272, 61, 6), (64, 528, 64, 8), (65, 1040, 65, 3),
-          (7, 5136, 130, 32), (300, 400, 257, 9), (2, 65536, 8, 2), (33, 256, 1000, 32), (700, 1024, 128, 8)]
+          (7, 5136, 130, 32), (300, 400, 257, 9), (2, 65536, 8, 2), (33, 256, 1000, 32), (700, 1024, 128, 8),
+          # matrix instructions: every count of experts per lane, both workgroups, ragged ends
+          (300, 2064, 61, 6), (17, 65536, 33, 1), (300, 2064, 257, 9), (100, 1040, 1000, 32), (2500, 272, 120, 8),
+          (1031, 144, 250, 1), (4096, 80, 128, 8), (600, 80, 1024, 32)]
 
 
 @pytest.mark.parametrize("normalize", [False, True])
@@ -174,7 +182,11 @@ def test_route(M, K, E, k, dtype, normalize):
     far = logits.max(1, keepdims=True) - np.take_along_axis(logits, oe, 1)
     if normalize:  # the sum's terms are off by theirs
         far = far + far.max(1, keepdims=True)
-    assert np.all(np.abs(f64(weights) - ow) <= (64 + far) * H * ow * 1.01 + 2.0 ** -149)
+    rel = (64 + far) * H * 1.01
+    if M * E * K > 2 ** 25:
+        b = 32 * 2.0 ** -23 * (np.abs(f64(x)) @ np.abs(f64(w)).T).max(1, keepdims=True)
+        rel = rel + np.expm1(2 * b * (2 if normalize else 1))
+    assert np.all(np.abs(f64(weights) - ow) <= rel * ow + 2.0 ** -149)
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
@@ -195,10 +207,25 @@ def test_route_close_logits(M, dtype):
     assert np.array_equal(experts.cpu().numpy(), np.repeat(want[None], M, 0))
 
 
+@pytest.mark.parametrize("scale", [(100, 40), (-100, -30)], ids=["large", "small"])
+@pytest.mark.parametrize("M", [3, 100])
+def test_route_outside_fp32(M, scale):
+    """Products that fp32 cannot hold, too large or too small: the order is that
+    of 64 bits all the same."""
+    K, E, k = 1040, 400, 8
+    x = (rows(M, K, torch.bfloat16, M, std=1.0, outliers=0).float() * 2.0 ** scale[0]).bfloat16()
+    w = (rows(E, K, torch.bfloat16, 2, std=1.0, outliers=0).float() * 2.0 ** scale[1]).bfloat16()
+    experts, weights = i8.moe_route(x, w, k, normalize=False)
+    oe, ow = O.route64(f64(x), f64(w), k, False)
+    assert np.array_equal(experts.cpu().numpy(), oe)
+    assert np.allclose(f64(weights), ow, rtol=64 * 2.0 ** -24, atol=2.0 ** -126)
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
-def test_route_bad_values(dtype):
+@pytest.mark.parametrize("M,K,E", [(6, 144, 70), (40, 4112, 230), (700, 1040, 70)])
+def test_route_bad_values(M, K, E, dtype):
     """NaN and infinite logits: experts stay distinct and in range; other rows stay."""
-    M, K, E, k = 6, 144, 70, 32
+    k = 32
     x, w = rows(M, K, dtype, 1), rows(E, K, dtype, 2, std=0.1)
     we, ww = i8.moe_route(x, w, k)
     x[1, 3] = float("nan")
@@ -209,7 +236,7 @@ def test_route_bad_values(dtype):
             assert sorted(set(e[m].tolist())) == sorted(e[m].tolist()) and 0 <= e[m].min() and e[m].max() < E
             assert torch.isnan(v[m]).any()
         assert e[1].tolist() == list(range(k)) and torch.isnan(v[1]).all()
-        keep = [0, 2, 4, 5]
+        keep = [0, 2, *range(4, M)]
         assert torch.equal(e[keep], we[keep])
         if normalize:
             assert torch.equal(v[keep], ww[keep])
