@@ -1,6 +1,6 @@
 """Torch modules over the C-ABI: an fp16 linear layer whose forward pass is
-the LLM.int8() decomposed matmul, and its block-scaled e4m3 counterpart with
-the norm that feeds it.
+the LLM.int8() decomposed matmul, its block-scaled e4m3 counterpart with the
+norms that feed it, and a mixture of experts with block-scaled e4m3 weights.
 
 The layer of the brain.gartu.xyz page's practical example ("Exemple
 pratique") replaces an nn.Linear (with bias) by an int8 layer with
@@ -12,9 +12,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (FP8_BLOCK, build_outlier_cache, fp8_matmul, fp8_pack_weight, fp8_quantize,
-               fp8_quantize_weight, fp8_rms_norm, mixed_matmul, mixed_matmul_cached,
-               quantize_weight, workspace_size)
+from . import (FP8_BLOCK, MOE_MAX_PAIRS, build_outlier_cache, fp8_matmul, fp8_moe, fp8_pack_experts,
+               fp8_pack_weight, fp8_quantize, fp8_quantize_weight, fp8_rms_norm, fp8_sandwich_norm,
+               mixed_matmul, mixed_matmul_cached, moe_route, quantize_weight, workspace_size)
 
 _HALVES = (torch.float16, torch.bfloat16)
 
@@ -125,6 +125,54 @@ class Fp8RMSNorm(torch.nn.Module):
         return (q, s), h.reshape(x.shape)
 
 
+class Fp8SandwichNorm(torch.nn.Module):
+    """The norm after a block, the residual's addition and the norm before the
+    next block: forward(x, residual, gate=None) for a block's output x gives
+    (y, h) with h = residual_scale * residual + gate * norm(x), the next residual,
+    and y = norm(h): with `quantize` the pair (e4m3, scales) that Fp8BlockLinear
+    layers take, else a tensor like x, as Fp8MoE takes it.  x [..., K] of the
+    weights' type, which half() and bfloat16() change; gate [K], or [G, K] with G
+    dividing the tokens, a row for each of G equal parts of them in turn.
+    """
+
+    def __init__(self, post_weight: torch.Tensor, pre_weight: torch.Tensor, eps: float = 1e-6,
+                 residual_scale: float = 1.0, quantize: bool = True):
+        super().__init__()
+        for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+            if w.dim() != 1 or w.device.type != "cuda":
+                raise TypeError(f"{name} must be a 1-D CUDA tensor")
+        if post_weight.shape != pre_weight.shape or post_weight.dtype != pre_weight.dtype:
+            raise ValueError("post_weight and pre_weight must have one shape and type")
+        self.register_buffer("post_weight", post_weight.detach().clone())
+        self.register_buffer("pre_weight", pre_weight.detach().clone())
+        self.eps, self.residual_scale = float(eps), float(residual_scale)
+        self.quantize = bool(quantize)
+
+    def _apply(self, fn, recurse=True):
+        # as Fp8RMSNorm: float() and the like only move the weights
+        held = {"post_weight": self.post_weight, "pre_weight": self.pre_weight}
+        super()._apply(fn, recurse)
+        for name, t in held.items():
+            now = getattr(self, name)
+            if now.dtype != t.dtype and now.dtype not in _HALVES:
+                setattr(self, name, t.to(now.device))
+        return self
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor, gate: torch.Tensor | None = None):
+        K = self.post_weight.numel()
+        if x.shape[-1] != K:
+            raise ValueError(f"expected last dimension {K}, got {x.shape[-1]}")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual {tuple(residual.shape)}, x {tuple(x.shape)}")
+        out = fp8_sandwich_norm(x.reshape(-1, K).contiguous(), residual.reshape(-1, K).contiguous(),
+                                self.post_weight, self.pre_weight,
+                                gate=None if gate is None else gate.contiguous(),
+                                residual_scale=self.residual_scale, eps=self.eps,
+                                quantize=self.quantize)
+        y = out[:2] if self.quantize else out[0].reshape(x.shape)
+        return y, out[-1].reshape(x.shape)
+
+
 class Fp8BlockLinear(torch.nn.Module):
     """y = x . W^T + b with block-scaled e4m3 weights (quantized once, when the
     module is built) and activations (quantized per call).
@@ -213,4 +261,104 @@ class Fp8BlockLinear(torch.nn.Module):
         return y.reshape(*x.shape[:-1], self.out_features)
 
 
-__all__ = ["Int8MixedLinear", "Fp8BlockLinear", "Fp8RMSNorm"]
+class Fp8MoE(torch.nn.Module):
+    """A mixture of experts with gated feed-forwards, for few tokens at a time: y
+    = sum over a token's top_k experts, by the router, of p_e * D_e (silu(G_e x) *
+    U_e x).  x [..., K] fp16 or bf16, y like x.  Built from fp16 or bf16 weights as
+    linear layers hold them, router [E, K], gate_up [E, 2I, K] (I gates, then I
+    ups) and down [E, K, I], the experts' quantized once, or by from_quantized
+    from a checkpoint's e4m3 ones.  `normalize`: a token's weights sum to 1.
+
+    Buffers: router (of x's type; half() and bfloat16() change it), gate_up,
+    gate_up_scale, down, down_scale.  For serving: y carries no gradient.  More
+    than MOE_MAX_PAIRS places of tokens are run in several calls.
+    """
+
+    def __init__(self, router: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, top_k: int,
+                 normalize: bool = True):
+        super().__init__()
+        self._check_shapes(router, gate_up, down)
+        for name, w in (("gate_up", gate_up), ("down", down)):
+            if w.dtype not in _HALVES:
+                raise TypeError(f"{name} must be fp16 or bf16, got {w.dtype}")
+        held = []
+        for w in (gate_up, down):
+            # one expert at a time: a transposed copy of all would double the memory
+            parts = [fp8_quantize_weight(w[e].detach().t().contiguous()) for e in range(w.shape[0])]
+            held += [torch.stack([q.view(torch.uint8) for q, _ in parts]).view(torch.float8_e4m3fn),
+                     torch.stack([s for _, s in parts])]
+        self._set(router, *held, top_k, normalize)
+
+    @staticmethod
+    def _check_shapes(router, gate_up, down):
+        if router.dim() != 2 or gate_up.dim() != 3 or down.dim() != 3:
+            raise TypeError("router must be [E, K], gate_up [E, 2I, K] and down [E, K, I]")
+        (E, K), I2 = router.shape, gate_up.shape[1]
+        if E < 1 or I2 % 2 or gate_up.shape != (E, I2, K) or down.shape != (E, K, I2 // 2):
+            raise ValueError(f"router {tuple(router.shape)}, gate_up {tuple(gate_up.shape)} and down "
+                             f"{tuple(down.shape)} do not fit as [E, K], [E, 2I, K] and [E, K, I]")
+        if router.dtype not in _HALVES:
+            raise TypeError(f"router must be fp16 or bf16, got {router.dtype}")
+        if any(t.device.type != "cuda" for t in (router, gate_up, down)):
+            raise TypeError("router, gate_up and down must be CUDA tensors")
+
+    def _set(self, router, gate_up, gate_up_scale, down, down_scale, top_k, normalize):
+        if not 1 <= top_k <= router.shape[0]:
+            raise ValueError(f"top_k must be 1 to {router.shape[0]}, got {top_k}")
+        self.register_buffer("router", router.detach().clone())
+        for name, t in (("gate_up", gate_up), ("gate_up_scale", gate_up_scale), ("down", down),
+                        ("down_scale", down_scale)):
+            self.register_buffer(name, t)
+        self.top_k, self.normalize = int(top_k), bool(normalize)
+
+    @classmethod
+    def from_quantized(cls, router: torch.Tensor, gate_up: torch.Tensor, gate_up_scale: torch.Tensor,
+                       down: torch.Tensor, down_scale: torch.Tensor, top_k: int,
+                       normalize: bool = True) -> "Fp8MoE":
+        """A checkpoint's e4m3 experts, gate_up [E, 2I, K] and down [E, K, I], with
+        their scales [E, ceil(2I/128), ceil(K/128)] and [E, ceil(K/128), ceil(I/128)]."""
+        cls._check_shapes(router, gate_up, down)
+        scales = []
+        for name, w, s in (("gate_up_scale", gate_up, gate_up_scale), ("down_scale", down, down_scale)):
+            blocks = (w.shape[0], *((n + FP8_BLOCK - 1) // FP8_BLOCK for n in w.shape[1:]))
+            if s.shape != blocks:
+                raise ValueError(f"{name} must have shape {blocks}, got {tuple(s.shape)}")
+            scales.append(s.detach().to(device=w.device, dtype=torch.float32).contiguous())
+        self = cls.__new__(cls)
+        torch.nn.Module.__init__(self)
+        self._set(router, fp8_pack_experts(gate_up.detach().contiguous()), scales[0],
+                  fp8_pack_experts(down.detach().contiguous()), scales[1], top_k, normalize)
+        return self
+
+    def _apply(self, fn, recurse=True):
+        # half() and bfloat16() change the router's type, float() and the like only
+        # move it; the e4m3 numbers and their fp32 scales only follow to another device
+        held = dict(self.named_buffers(recurse=False))
+        super()._apply(fn, recurse)
+        for name, t in held.items():
+            now = getattr(self, name)
+            if now.dtype != t.dtype and not (name == "router" and now.dtype in _HALVES):
+                setattr(self, name, t.to(now.device))
+        return self
+
+    def extra_repr(self) -> str:
+        E, K = self.router.shape
+        return (f"features={K}, experts={E}, expert_features={self.gate_up.shape[1] // 2}, "
+                f"top_k={self.top_k}, normalize={self.normalize}")
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        K = self.router.shape[1]
+        if x.shape[-1] != K:
+            raise ValueError(f"expected last dimension {K}, got {x.shape[-1]}")
+        x2 = x.reshape(-1, K).contiguous()
+        experts, weights = moe_route(x2, self.router, self.top_k, normalize=self.normalize)
+        most = MOE_MAX_PAIRS // self.top_k
+        y = torch.empty_like(x2)
+        for m in range(0, max(1, x2.shape[0]), most):
+            part = slice(m, m + most)
+            fp8_moe(x2[part], experts[part], weights[part], self.gate_up, self.gate_up_scale, self.down,
+                    self.down_scale, out=y[part])
+        return y.reshape(x.shape)
+
+
+__all__ = ["Int8MixedLinear", "Fp8BlockLinear", "Fp8RMSNorm", "Fp8SandwichNorm", "Fp8MoE"]

@@ -13,6 +13,8 @@ fp8.py.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _check, load
@@ -23,6 +25,17 @@ __all__ = ["MOE_MAX_PAIRS", "moe_route", "fp8_moe", "fp8_pack_experts", "fp8_qua
 
 MOE_MAX_PAIRS = 8192  # tokens * top_k of one fp8_moe call
 _I32, _F32 = (torch.int32,), (torch.float32,)
+
+
+# a foreign call of 1 us for what a loop asks again and again
+@functools.lru_cache(maxsize=256)
+def _route_bytes(M, K, E, top_k):
+    return load().moe_route_workspace_size(M, K, E, top_k)
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_bytes(M, K, I, E, top_k):
+    return load().fp8_moe_workspace_size(M, K, I, E, top_k)
 
 
 def fp8_pack_experts(Wq: torch.Tensor, stream=None) -> torch.Tensor:
@@ -82,11 +95,10 @@ def moe_route(X: torch.Tensor, W: torch.Tensor, top_k: int, normalize: bool = Tr
     else:
         experts = _tensor(out[0], "out[0]", _I32, (M, top_k), dev)
         weights = _tensor(out[1], "out[1]", _F32, (M, top_k), dev)
-    lib = load()
-    size = lib.moe_route_workspace_size(M, K, E, top_k)
+    size = _route_bytes(M, K, E, top_k)
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    _check(lib.moe_route(_at(X), _at(W), _TYPES[X.dtype], M, K, E, top_k, bool(normalize),
-                         _at(experts), _at(weights), _at(ws), size, _stream_of(X.get_device())))
+    _check(load().moe_route(_at(X), _at(W), _TYPES[X.dtype], M, K, E, top_k, bool(normalize),
+                            _at(experts), _at(weights), _at(ws), size, _stream_of(X.get_device())))
     return experts, weights
 
 
@@ -110,11 +122,11 @@ def fp8_moe(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, gate_
     if experts.shape[0] != M:
         raise ValueError(f"experts has {experts.shape[0]} rows, X {M}")
     _tensor(weights, "weights", _F32, (M, top_k), dev)
-    E, I2, _ = _tensor(gate_up, "gate_up", (_E4M3,), 3, dev).shape
-    if I2 % 2:
-        raise ValueError(f"gate_up must have an even number of rows, got {I2}")
+    E, I2, columns = _tensor(gate_up, "gate_up", (_E4M3,), 3, dev).shape
+    if I2 % 2 or columns != fp8_kpad(K):
+        raise ValueError(f"gate_up must have an even number of rows and {fp8_kpad(K)} columns, "
+                         f"got {I2} and {columns}")
     I = I2 // 2
-    _tensor(gate_up, "gate_up", (_E4M3,), (E, I2, fp8_kpad(K)), dev)
     _tensor(gate_up_scale, "gate_up_scale", _F32, (E, _blocks(I2), _blocks(K)), dev)
     _tensor(down, "down", (_E4M3,), (E, K, fp8_kpad(I)), dev)
     _tensor(down_scale, "down_scale", _F32, (E, _blocks(K), _blocks(I)), dev)
@@ -122,10 +134,9 @@ def fp8_moe(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, gate_
         out = torch.empty_like(X)
     else:
         _tensor(out, "out", (X.dtype,), (M, K), dev)
-    lib = load()
-    size = lib.fp8_moe_workspace_size(M, K, I, E, top_k)
+    size = _moe_bytes(M, K, I, E, top_k)
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    _check(lib.fp8_moe(_at(X), _TYPES[X.dtype], M, K, _at(experts), _at(weights), top_k, _at(gate_up),
-                       _at(gate_up_scale), _at(down), _at(down_scale), I, E, _at(out), _at(ws), size,
-                       _stream_of(X.get_device())))
+    _check(load().fp8_moe(_at(X), _TYPES[X.dtype], M, K, _at(experts), _at(weights), top_k,
+                          _at(gate_up), _at(gate_up_scale), _at(down), _at(down_scale), I, E,
+                          _at(out), _at(ws), size, _stream_of(X.get_device())))
     return out
