@@ -133,16 +133,22 @@ hipError_t run(const SandwichCall& c, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Threads and chunks of 8 columns per thread that hold a row of K <= 65536.
+// Threads and chunks of 8 columns per thread that hold a row of K <= 65536.  Two
+// or three chunks per thread let more rows share a CU than one (us, calls in a
+// graph, bf16: 4096x4096, 512 x 1 and 256 x 2: 23.3 and 22.1; 2048x5120, 640 x 1,
+// 512 x 2, 384 x 2, 256 x 3: 20.4, 18.7, 18.1, 16.8; 4096x12288, 768 x 2, 512 x 3,
+// 384 x 4, 256 x 6: 81.2, 77.4, 83.4, 82.7 = 4.6 TB/s); a few rows wait for one
+// row's latency (1x5120, 384 x 2 and 256 x 3: 6.0 and 6.6).
 template <int T>
 hipError_t shape(const SandwichCall& c, hipStream_t st) {
   const int chunks = (c.K + 7) / 8;
   if (chunks <= 64) return run<T, 64, 1>(c, st);
   if (chunks <= 128) return run<T, 128, 1>(c, st);
   if (chunks <= 256) return run<T, 256, 1>(c, st);
-  if (chunks <= 512) return run<T, 512, 1>(c, st);
-  if (chunks <= 1024) return run<T, 512, 2>(c, st);
-  if (chunks <= 1536) return run<T, 768, 2>(c, st);
+  if (chunks <= 512) return run<T, 256, 2>(c, st);
+  if (chunks <= 768)
+    return c.M <= 2 * device_cu_count() ? run<T, 384, 2>(c, st) : run<T, 256, 3>(c, st);
+  if (chunks <= 1536) return run<T, 512, 3>(c, st);
   if (chunks <= 2048) return run<T, 1024, 2>(c, st);
   if (chunks <= 4096) return run<T, 1024, 4>(c, st);
   return run<T, 1024, 8>(c, st);

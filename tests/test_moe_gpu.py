@@ -83,7 +83,9 @@ def norm_bounds(x, r, post, pre, gate, alpha, eps):
 
 
 NORMS = [(1, 16, 0), (1, 128, 1), (3, 112, 3), (4, 528, 2), (17, 1040, 0), (6, 2064, 6), (12, 4112, 4), (1, 5120, 1),
-         (5, 8208, 5), (33, 12288, 1), (2, 16400, 2), (2, 32784, 0), (2, 65536, 1)]
+         (5, 8208, 5), (33, 12288, 1), (2, 16400, 2), (2, 32784, 0), (2, 65536, 1),
+         # a row's every count of threads and chunks, many rows too
+         (2, 512, 1), (2, 1024, 0), (2, 2048, 2), (2, 4096, 1), (600, 5136, 600), (2, 6144, 0), (520, 12304, 1)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
