@@ -371,18 +371,20 @@ __global__ __launch_bounds__(KS * 64) void k_moe_down(MoeCall c) {
 // ---- many workgroups: no split of the columns --------------------------------
 //
 // A workgroup's eight wavefronts take two blocks of 16 weight rows each, over all
-// columns, and share the tokens' tile of a 128-column block in LDS (two stages;
-// the next one travels through registers under the products of this one).  The
-// weights go straight to the wavefront that uses them, up to two blocks ahead.
+// columns, and share the tokens' tile of a 128-column block in LDS, which comes by
+// DMA a block ahead (two blocks ahead it took as long: 512x4096 of 128 experts
+// 541 and 546 us).  The weights go straight to the wavefront that uses them, up to
+// two blocks ahead.
 // A tile row is 256 bytes per number of an operand column, its 16-byte chunks
-// swapped by the row's low three bits so that eight rows' reads of one chunk
-// meet all banks.
+// swapped by the row's low four bits: a read of 16 bytes serves 16 lanes at once,
+// eight of one chunk and eight of the next one, and they meet all 64 banks (by
+// three bits, half of the reads' cycles were conflicts).
 template <int TY, int T, int PLANES>
 struct Wide {
   static constexpr int WAVES = 8, NB = 2, NT = WAVES * 64;
   static constexpr int ROW = 256 * PLANES, CHUNKS = ROW / 16;
   static constexpr int STAGE = T * 16 * ROW;
-  static constexpr int LOADS = (T * 16 * CHUNKS + NT - 1) / NT;
+  static constexpr int LOADS = (T * 16 * CHUNKS + NT - 1) / NT;  // DMAs of a wavefront
   typedef const __attribute__((address_space(4))) float* scalar_ptr;
   struct Weights {
     v4i w[NB][2];
@@ -408,7 +410,7 @@ struct Wide {
     // The tile's chunk number i * NT + thread of LDS holds the swapped chunk of its row.
     uint32_t src[LOADS];
     const int slot = tid % CHUNKS, row0 = tid / CHUNKS;
-    const int c = slot ^ (row0 & 7);  // NT / CHUNKS rows further the low bits are the same
+    const int c = slot ^ (row0 & 15);  // NT / CHUNKS rows further the low bits are the same
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int j = j0 + row0 + i * (NT / CHUNKS);
@@ -457,7 +459,7 @@ struct Wide {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int c = (h * 4 + q4) * 2 * PLANES + p * 2 + i;
-              const v4i f = *reinterpret_cast<const v4i*>(row + (c ^ (r16 & 7)) * 16);
+              const v4i f = *reinterpret_cast<const v4i*>(row + (c ^ r16) * 16);
 #pragma unroll
               for (int b = 0; b < NB; ++b) sum[b] = mfma32<TY>(w[h][b][i], f, sum[b]);
             }
@@ -475,19 +477,18 @@ struct Wide {
       for (int t = 0; t < T; ++t) acc[b][t] = v4f{};
     if (KB == 0) return;
     Weights a, b;
+    constexpr int WOPS = 2 * NB;  // vector loads of a block's weights
     load_x(0, 0);
     load_w(0, a);
     load_w(min(1, KB - 1), b);
-    constexpr int WOPS = 2 * NB;  // vector loads of a block's weights
-    barrier_vm<2 * WOPS>();       // the tile is there
+    barrier_vm<2 * WOPS>();  // the first tile is there
     auto step = [&](int kb, Weights& cur) {
       const int stage = kb & 1;
       load_x(min(kb + 1, KB - 1), stage ^ 1);
       __builtin_amdgcn_sched_barrier(0);
       compute(cur, stage);
       load_w(min(kb + 2, KB - 1), cur);
-      // the next tile is there, and this one free
-      barrier_vm<WOPS>();
+      barrier_vm<WOPS>();  // the next tile is there, and this one free
     };
     for (int kb = 0; kb < KB; kb += 2) {
       step(kb, a);
@@ -565,28 +566,30 @@ __device__ __forceinline__ void down_wide(const MoeCall& c, int e, int j0, int n
   }
 }
 
-// UP: the first product, else the second.  Up to 16 * TMAX of an expert's tokens
-// per pass over its weights.
-template <int TY, bool UP, int TMAX>
-__global__ __launch_bounds__(512, TMAX == 1 ? 6 : 4) void k_moe_wide(MoeCall c) {
+// Bytes of LDS for the two tiles of the most tokens.
+template <int PLANES>
+constexpr int kWideLds = 2 * Wide<kF16, 4, PLANES>::STAGE;
+
+// UP: the first product, else the second.  Up to 64 of an expert's tokens per
+// pass over its weights.
+template <int TY, bool UP>
+__global__ __launch_bounds__(512, 4) void k_moe_wide(MoeCall c) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int counts[8];
-  constexpr int TILE = 2 * Wide<TY, TMAX, UP ? 1 : 2>::STAGE;
+  constexpr int TILE = kWideLds<UP ? 1 : 2>;
   uint16_t* list = reinterpret_cast<uint16_t*>(smem + TILE);
   int n;
   const int e = expert_of_slot<512>(c, blockIdx.y, list, counts, n);
   if (e < 0) return;
   auto pass = [&](auto t, int j0) {
-    if constexpr (t() <= TMAX) {
-      if constexpr (UP)
-        up_wide<TY, t()>(c, e, j0, n, list, smem);
-      else
-        down_wide<t()>(c, e, j0, n, list, smem);
-    }
+    if constexpr (UP)
+      up_wide<TY, t()>(c, e, j0, n, list, smem);
+    else
+      down_wide<t()>(c, e, j0, n, list, smem);
   };
-  for (int j0 = 0; j0 < n; j0 += 16 * TMAX) {
-    const int blocks = min((n - j0 + 15) / 16, TMAX);
-    if (blocks == 4)
+  for (int j0 = 0; j0 < n; j0 += 64) {
+    const int blocks = (n - j0 + 15) / 16;
+    if (blocks >= 4)
       pass(std::integral_constant<int, 4>{}, j0);
     else if (blocks == 3)
       pass(std::integral_constant<int, 3>{}, j0);
@@ -873,25 +876,32 @@ hipError_t launch_big(Kernel kern, std::atomic<uint64_t>& asked, dim3 grid, int 
 }
 
 template <int TY, int TMAX>
-hipError_t run_split(const MoeCall& c, int slots, hipStream_t st) {
-  constexpr int KSU = TMAX == 1 ? 8 : 4, KSD = 4, NB = 2;
-  const size_t list = (size_t)c.M * c.top_k * 2;
-  if (c.I > 0)
-    k_moe_up<TY, TMAX, KSU><<<dim3(c.I / 16, slots), KSU * 64, KSU * 2 * TMAX * 1024 + list, st>>>(c);
-  k_moe_down<NB, TMAX, KSD>
-      <<<dim3((c.K / 16 + NB - 1) / NB, slots), KSD * 64, KSD * NB * TMAX * 1024 + list, st>>>(c);
+hipError_t split_up(const MoeCall& c, int slots, hipStream_t st) {
+  constexpr int KS = TMAX == 1 ? 8 : 4;
+  k_moe_up<TY, TMAX, KS><<<dim3(c.I / 16, slots), KS * 64,
+                           KS * 2 * TMAX * 1024 + (size_t)c.M * c.top_k * 2, st>>>(c);
   return hipGetLastError();
 }
 
-template <int TY, int TMAX>
-hipError_t run_wide(const MoeCall& c, int slots, hipStream_t st) {
-  static std::atomic<uint64_t> asked[2];
-  const size_t list = (size_t)c.M * c.top_k * 2;
-  hipError_t e = launch_big(k_moe_wide<TY, true, TMAX>, asked[0], dim3((c.I / 16 + 7) / 8, slots),
-                            512, 2 * Wide<TY, TMAX, 1>::STAGE + list, c, st);
-  if (e != hipSuccess) return e;
-  return launch_big(k_moe_wide<kBf16, false, TMAX>, asked[1], dim3((c.K / 16 + 15) / 16, slots),
-                    512, 2 * Wide<TY, TMAX, 2>::STAGE + list, c, st);
+template <int TMAX>
+hipError_t split_down(const MoeCall& c, int slots, hipStream_t st) {
+  constexpr int KS = 4, NB = 2;
+  k_moe_down<NB, TMAX, KS><<<dim3((c.K / 16 + NB - 1) / NB, slots), KS * 64,
+                             KS * NB * TMAX * 1024 + (size_t)c.M * c.top_k * 2, st>>>(c);
+  return hipGetLastError();
+}
+
+template <int TY>
+hipError_t wide_up(const MoeCall& c, int slots, hipStream_t st) {
+  static std::atomic<uint64_t> asked;
+  return launch_big(k_moe_wide<TY, true>, asked, dim3((c.I / 16 + 7) / 8, slots), 512,
+                    kWideLds<1> + (size_t)c.M * c.top_k * 2, c, st);
+}
+
+inline hipError_t wide_down(const MoeCall& c, int slots, hipStream_t st) {
+  static std::atomic<uint64_t> asked;
+  return launch_big(k_moe_wide<kBf16, false>, asked, dim3((c.K / 16 + 15) / 16, slots), 512,
+                    kWideLds<2> + (size_t)c.M * c.top_k * 2, c, st);
 }
 
 // Whether each pair goes alone: one token, or so few pairs that they seldom
@@ -920,10 +930,23 @@ hipError_t run(const MoeCall& c, hipStream_t st) {
   if (few_pairs(c)) return run_few<TY>(c, st);
   hipError_t e = hipSuccess;
   if (slots > 0) {
-    if (c.M <= 16)
-      e = run_split<TY, 1>(c, slots, st);
+    if (c.I > 0) {
+      // U: the first product.  Few tokens per expert, or none beyond 16: the columns
+      // split, 16 tokens at a time; else tiles, if they fill half of the chip.
+      if (c.M <= 16 || P < 5 * c.E)
+        e = split_up<TY, 1>(c, slots, st);
+      else if (2 * (int64_t)slots * ((c.I + 127) / 128) > device_cu_count())
+        e = wide_up<TY>(c, slots, st);
+      else
+        e = split_up<TY, 4>(c, slots, st);
+      if (e != hipSuccess) return e;
+    }
+    if ((int64_t)slots * ((c.K + 255) / 256) >= 2 * device_cu_count())
+      e = wide_down(c, slots, st);
+    else if (P > 64 * slots && c.I >= 8 * kFp8Block)
+      e = split_down<4>(c, slots, st);
     else
-      e = c.I > 0 ? run_wide<TY, 4>(c, slots, st) : run_split<TY, 4>(c, slots, st);
+      e = split_down<1>(c, slots, st);
   }
   if (e != hipSuccess) return e;
   k_moe_join<TY><<<(unsigned)(((int64_t)c.M * (c.K / 8) + 255) / 256), 256, 0, st>>>(c);
