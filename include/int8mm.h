@@ -538,7 +538,8 @@ size_t fp8_moe_workspace_size(int64_t M, int64_t K, int64_t I, int64_t E, int64_
  * fp8_moe -- the experts of each token:
  *     a[p] = silu(X[m] . G_e^T) * (X[m] . U_e^T)    for the pairs p = (m, j), e = experts[p]
  *     Y[m] = sum over j of weights[p] * (a[p] . D_e^T)
- * with fp32 sums, the pairs of a token added in the order of j, rounded once.
+ * with fp32 sums, the pairs of a token added in the order of j, rounded once (a
+ * between the products is held to 2^-17; silu as in fp8_silu_mul).
  * Each expert that some token has is read once for (up to 64 of) its tokens,
  * so the call is made for few tokens per expert.
  *   X              in  [M][K], 16-bit, Y out [M][K] of the same type.

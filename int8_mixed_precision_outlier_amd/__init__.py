@@ -27,7 +27,8 @@ __all__ = [
     "STATUS_OK", "STATUS_EINVAL", "STATUS_EALIGN", "STATUS_EWORKSPACE", "STATUS_EHIP",
     "FP8_BLOCK", "fp8_kpad", "fp8_pack_weight", "fp8_quantize_weight", "fp8_quantize",
     "fp8_rms_norm", "fp8_sandwich_norm", "fp8_silu_mul", "fp8_matmul", "fp8_matmul_config",
-    "moe_route", "fp8_moe", "fp8_pack_experts", "fp8_quantize_experts", "MOE_MAX_PAIRS",
+    "moe_route", "fp8_moe", "fp8_pack_experts", "fp8_quantize_experts",
+    "MOE_MAX_EXPERTS", "MOE_MAX_TOP_K", "MOE_MAX_PAIRS",
     "STATUS_ESCRATCH", "FLAG_OVERFLOW", "FLAG_CACHE_MISS", "FLAG_CACHE_MISMATCH",
 ]
 
@@ -517,5 +518,5 @@ def timing_read():
 
 from .fp8 import (FP8_BLOCK, fp8_kpad, fp8_matmul, fp8_matmul_config, fp8_pack_weight,  # noqa: E402
                   fp8_quantize, fp8_quantize_weight, fp8_rms_norm, fp8_sandwich_norm, fp8_silu_mul)
-from .moe import (MOE_MAX_PAIRS, fp8_moe, fp8_pack_experts, fp8_quantize_experts,  # noqa: E402
-                  moe_route)
+from .moe import (MOE_MAX_EXPERTS, MOE_MAX_PAIRS, MOE_MAX_TOP_K, fp8_moe,  # noqa: E402
+                  fp8_pack_experts, fp8_quantize_experts, moe_route)

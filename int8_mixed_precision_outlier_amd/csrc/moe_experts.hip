@@ -97,11 +97,13 @@ __device__ __forceinline__ int expert_of_slot(const MoeCall& c, int s, uint16_t*
   return e;
 }
 
-// One product of NB blocks of 16 weight rows with T blocks of 16 tokens over
-// the wavefront's K blocks w, w + KS, ...
-//   w_row[b]   row block of the expert's packed matrix
-//   rows[t]    byte offset of the lane's token in the operand, or kNoRow
-// The operand holds `PLANES` numbers per column that are added: 16 columns are
+// ---- the columns split over a workgroup's wavefronts -------------------------
+//
+// One product of NB blocks of 16 weight rows (at bytes w_at[b] of the expert's
+// packed matrix, with scales s_at[b]) with T blocks of 16 tokens (rows[t]: byte
+// offset of the lane's token in the operand, or kNoRow) over the wavefront's
+// 128-column blocks w, w + KS, ...  Weights and tokens come straight to registers,
+// a block ahead.  The operand holds `PLANES` numbers per column that are added: 16 columns are
 // 32 bytes of the first, then 32 of the second.
 template <int TY, int NB, int T, int PLANES, int KS>
 struct Product {
@@ -207,8 +209,8 @@ struct Product {
   }
 };
 
-// The sums of the wavefronts' partial products, in wavefront order; `red` is
-// [KS][NB * T][64] v4f of LDS.  Leaves tile o = b * T + t with any wavefront.
+// The wavefronts' sums through LDS, [KS][NB * T][64]: any wavefront can then add
+// those of tile o = b * T + t, in wavefront order.
 template <int NB, int T, int KS>
 __device__ __forceinline__ void spread_partials(const v4f (&acc)[NB][T], int w, int lane, v4f* red) {
 #pragma unroll
@@ -278,9 +280,7 @@ __device__ __forceinline__ void up_tokens(const MoeCall& c, int e, int j0, int n
   for (int t = w; t < T; t += KS) {
     const v4f g = joined<2, T, KS>(red, t, lane), u = joined<2, T, KS>(red, T + t, lane);
     const int j = j0 + t * 16 + r16;
-    if (j < n) {
-      store_gated(g, u, c.act + ((size_t)list[j] * c.I + f * 16) * 4 + q4 * 8);
-    }
+    if (j < n) store_gated(g, u, c.act + ((size_t)list[j] * c.I + f * 16) * 4 + q4 * 8);
   }
   __syncthreads();  // `red` is free
 }
@@ -605,8 +605,11 @@ __global__ __launch_bounds__(512, 4) void k_moe_wide(MoeCall c) {
 // With far fewer pairs than experts an expert has hardly ever two tokens, so each
 // pair goes alone, without matrix instructions: a lane multiplies its 16 numbers
 // of a row by the pair's activations (fp32, in LDS, read by 16 lanes at once).
-// That needs one accumulator and no operand registers, so CB blocks of weights
-// are on their way at once; what these calls wait for is latency.
+// That needs one accumulator a row block and no operand registers, so that many
+// wavefronts fit a CU with CB blocks of weights on their way each, refilled as
+// they are used; these calls wait for latency (1x4096 of 128 experts, 8 places of
+// 1408: 29.5 us in a graph, 17 + 10 in the two kernels = 5.2 TB/s; CB = 4 and 6,
+// without the order of the reads below, 32).
 
 // The sums over columns [kb0, kb1) * 128 of NB row blocks; lane l has that of row
 // l % 16 in every of its four quarters.  x.load(kb) starts the loads of the
@@ -755,7 +758,7 @@ __global__ __launch_bounds__(kFewUpWaves * 64) void k_moe_up_few(MoeCall c) {
 }
 
 // Second product and the sum over the pairs: a workgroup owns 16 features of all
-// pairs; its wavefronts take the pairs in turn, or, where there are fewer pairs,
+// pairs, so nothing is joined in another launch; its wavefronts take the pairs in turn, or, where there are fewer pairs,
 // one of `parts` shares of a pair's columns.
 constexpr int kFewDownWaves = 16, kFewDownBlocks = 2;
 constexpr int kFewPairs = 64;
@@ -924,30 +927,43 @@ hipError_t run_few(const MoeCall& c, hipStream_t st) {
   return hipGetLastError();
 }
 
+// First product, us of a call in a graph (tokens x columns, expert's width,
+// experts, places):
+//   up to 4 tokens an expert, or 16 in all: the columns split, 16 tokens at a time,
+//     against shared tiles: 64x4096 1408 128 8: 358 and 373, 48x5120 1408 64 6: 231
+//     and 253 (96x4096 1408 128 8, 6 tokens an expert: 425 and 401);
+//   else shared tiles, where their workgroups are more than half of the CUs,
+//     against the columns split and 64 tokens at a time: 364x720 1824 12 5: 137 and
+//     157, 385x7008 608 114 4: 368 and 396 (128x4096 512 8 2, 32 workgroups: 66 and 41).
+template <int TY>
+hipError_t first_product(const MoeCall& c, int slots, hipStream_t st) {
+  if (c.M <= 16 || c.M * c.top_k < 5 * c.E) return split_up<TY, 1>(c, slots, st);
+  if (2 * (int64_t)slots * ((c.I + 127) / 128) > device_cu_count())
+    return wide_up<TY>(c, slots, st);
+  return split_up<TY, 4>(c, slots, st);
+}
+
+// Second product, the same way:
+//   shared tiles, where their workgroups fill the chip once, against the columns
+//     split and 16 tokens at a time: 385x7008 608 114 4: 368 and 510, 24x4096 1408
+//     128 8: 268 and 279 (32x5120 8192 8 2, 160 workgroups: 201 and 199, 8x5120
+//     8192 8 2: 177 and 156);
+//   else the columns split: 64 tokens at a time for many tokens an expert, and
+//     columns to split, against 16: 364x720 1824 12 5: 137 and 158, 200x256 2816 4
+//     2: 70 and 76 (132x1904 144 9 7, two column blocks: 54 and 47).
+hipError_t second_product(const MoeCall& c, int slots, hipStream_t st) {
+  if ((int64_t)slots * ((c.K + 255) / 256) >= 2 * device_cu_count())
+    return wide_down(c, slots, st);
+  if (c.M * c.top_k > 64 * slots && c.I >= 8 * kFp8Block) return split_down<4>(c, slots, st);
+  return split_down<1>(c, slots, st);
+}
+
 template <int TY>
 hipError_t run(const MoeCall& c, hipStream_t st) {
   const int P = c.M * c.top_k, slots = P < c.E ? P : c.E;
   if (few_pairs(c)) return run_few<TY>(c, st);
-  hipError_t e = hipSuccess;
-  if (slots > 0) {
-    if (c.I > 0) {
-      // U: the first product.  Few tokens per expert, or none beyond 16: the columns
-      // split, 16 tokens at a time; else tiles, if they fill half of the chip.
-      if (c.M <= 16 || P < 5 * c.E)
-        e = split_up<TY, 1>(c, slots, st);
-      else if (2 * (int64_t)slots * ((c.I + 127) / 128) > device_cu_count())
-        e = wide_up<TY>(c, slots, st);
-      else
-        e = split_up<TY, 4>(c, slots, st);
-      if (e != hipSuccess) return e;
-    }
-    if ((int64_t)slots * ((c.K + 255) / 256) >= 2 * device_cu_count())
-      e = wide_down(c, slots, st);
-    else if (P > 64 * slots && c.I >= 8 * kFp8Block)
-      e = split_down<4>(c, slots, st);
-    else
-      e = split_down<1>(c, slots, st);
-  }
+  hipError_t e = c.I > 0 ? first_product<TY>(c, slots, st) : hipSuccess;
+  if (e == hipSuccess) e = second_product(c, slots, st);
   if (e != hipSuccess) return e;
   k_moe_join<TY><<<(unsigned)(((int64_t)c.M * (c.K / 8) + 255) / 256), 256, 0, st>>>(c);
   return hipGetLastError();

@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (FP8_BLOCK, MOE_MAX_PAIRS, build_outlier_cache, fp8_matmul, fp8_moe, fp8_pack_experts,
+from . import (FP8_BLOCK, MOE_MAX_EXPERTS, MOE_MAX_PAIRS, MOE_MAX_TOP_K, build_outlier_cache, fp8_matmul, fp8_moe, fp8_pack_experts,
                fp8_pack_weight, fp8_quantize, fp8_quantize_weight, fp8_rms_norm, fp8_sandwich_norm,
                mixed_matmul, mixed_matmul_cached, moe_route, quantize_weight, workspace_size)
 
@@ -294,6 +294,8 @@ class Fp8MoE(torch.nn.Module):
         if router.dim() != 2 or gate_up.dim() != 3 or down.dim() != 3:
             raise TypeError("router must be [E, K], gate_up [E, 2I, K] and down [E, K, I]")
         (E, K), I2 = router.shape, gate_up.shape[1]
+        if E > MOE_MAX_EXPERTS:
+            raise ValueError(f"at most {MOE_MAX_EXPERTS} experts, got {E}")
         if E < 1 or I2 % 2 or gate_up.shape != (E, I2, K) or down.shape != (E, K, I2 // 2):
             raise ValueError(f"router {tuple(router.shape)}, gate_up {tuple(gate_up.shape)} and down "
                              f"{tuple(down.shape)} do not fit as [E, K], [E, 2I, K] and [E, K, I]")
@@ -303,8 +305,9 @@ class Fp8MoE(torch.nn.Module):
             raise TypeError("router, gate_up and down must be CUDA tensors")
 
     def _set(self, router, gate_up, gate_up_scale, down, down_scale, top_k, normalize):
-        if not 1 <= top_k <= router.shape[0]:
-            raise ValueError(f"top_k must be 1 to {router.shape[0]}, got {top_k}")
+        most = min(router.shape[0], MOE_MAX_TOP_K)
+        if not 1 <= top_k <= most:
+            raise ValueError(f"top_k must be 1 to {most}, got {top_k}")
         self.register_buffer("router", router.detach().clone())
         for name, t in (("gate_up", gate_up), ("gate_up_scale", gate_up_scale), ("down", down),
                         ("down_scale", down_scale)):
@@ -351,13 +354,13 @@ class Fp8MoE(torch.nn.Module):
         if x.shape[-1] != K:
             raise ValueError(f"expected last dimension {K}, got {x.shape[-1]}")
         x2 = x.reshape(-1, K).contiguous()
-        experts, weights = moe_route(x2, self.router, self.top_k, normalize=self.normalize)
-        most = MOE_MAX_PAIRS // self.top_k
         y = torch.empty_like(x2)
+        most = MOE_MAX_PAIRS // self.top_k
         for m in range(0, max(1, x2.shape[0]), most):
-            part = slice(m, m + most)
-            fp8_moe(x2[part], experts[part], weights[part], self.gate_up, self.gate_up_scale, self.down,
-                    self.down_scale, out=y[part])
+            part = x2[m:m + most]
+            experts, weights = moe_route(part, self.router, self.top_k, normalize=self.normalize)
+            fp8_moe(part, experts, weights, self.gate_up, self.gate_up_scale, self.down,
+                    self.down_scale, out=y[m:m + most])
         return y.reshape(x.shape)
 
 

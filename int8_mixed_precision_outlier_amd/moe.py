@@ -21,8 +21,9 @@ from . import _check, load
 from .fp8 import (_E4M3, _HALVES, _TYPES, _at, _blocks, _current, _elsewhere, _stream_of, _tensor,
                   fp8_kpad)
 
-__all__ = ["MOE_MAX_PAIRS", "moe_route", "fp8_moe", "fp8_pack_experts", "fp8_quantize_experts"]
+__all__ = ["MOE_MAX_EXPERTS", "MOE_MAX_TOP_K", "MOE_MAX_PAIRS", "moe_route", "fp8_moe", "fp8_pack_experts", "fp8_quantize_experts"]
 
+MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 1024, 32
 MOE_MAX_PAIRS = 8192  # tokens * top_k of one fp8_moe call
 _I32, _F32 = (torch.int32,), (torch.float32,)
 

@@ -300,7 +300,12 @@ class Case:
 SIZES = [(1, 16, 16, 1, 1), (1, 128, 128, 4, 2), (1, 1040, 272, 8, 2), (2, 144, 400, 300, 3), (3, 272, 16, 5, 5),
          (5, 528, 144, 16, 4), (16, 256, 656, 8, 2), (17, 400, 80, 7, 6), (33, 144, 272, 2, 2), (40, 272, 144, 64, 8),
          (64, 128, 128, 1, 1), (65, 144, 32, 2, 1), (130, 400, 144, 3, 2), (200, 144, 144, 40, 6), (600, 272, 48, 9, 4),
-         (12, 2064, 1168, 6, 2), (70, 1168, 1040, 5, 2)]
+         (12, 2064, 1168, 6, 2), (70, 1168, 1040, 5, 2),
+         # shared tiles of 1 to 4 blocks of tokens and several passes, first product, second, both
+         (100, 144, 1168, 16, 2), (250, 272, 1168, 16, 3), (400, 144, 1168, 16, 3), (60, 2064, 80, 60, 2),
+         (300, 1040, 272, 110, 8), (700, 2064, 144, 60, 6), (340, 1040, 272, 120, 16),
+         # the columns split, 64 tokens at a time
+         (90, 144, 1168, 1, 1), (150, 400, 1040, 2, 2), (33, 1040, 144, 3, 2)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
@@ -371,6 +376,46 @@ def test_moe_bad_values_stay(dtype):
     keep = [m for m in range(20) if m not in bad]
     assert torch.equal(Y[keep], want[keep])
     assert torch.isnan(Y[3]).all() and torch.isnan(Y[11]).all() and not torch.isfinite(Y[7]).any()
+
+
+# sizes that take each kernel: pairs alone, columns split, shared tiles
+KERNELS = [(1, 272, 144, 6, 2), (12, 272, 144, 6, 2), (400, 144, 1168, 16, 3), (340, 1040, 272, 120, 16),
+           (150, 400, 1040, 2, 2)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,K,I,E,k", KERNELS)
+def test_moe_bad_weights(M, K, I, E, k, dtype):
+    """A NaN among an expert's numbers reaches the tokens of that expert and no
+    others: all features from the first matrix, one from the second."""
+    c = Case(M, K, I, E, k, dtype, seed=17)
+    e = int(c.experts[0, 0])
+    hit = torch.from_numpy((c.experts == e).any(1)).cuda()
+    want = i8.fp8_moe(*c.gpu())
+    up = c.up.copy()
+    c.up[e, 2 * I - 1, K - 1] = 0x7f
+    Y = i8.fp8_moe(*c.gpu())
+    assert torch.isnan(Y[hit]).all() and torch.equal(Y[~hit], want[~hit])
+    c.up = up
+    c.down[e, K - 1, 0] = 0xff
+    Y = i8.fp8_moe(*c.gpu())
+    assert torch.isnan(Y[hit, K - 1]).all()
+    assert torch.equal(Y[:, :K - 1], want[:, :K - 1]) and torch.equal(Y[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,K,I,E,k", KERNELS)
+def test_moe_subnormal_activations(M, K, I, E, k, dtype):
+    """Activations below the type's normal numbers count as what they are."""
+    c = Case(M, K, I, E, k, dtype, seed=19)
+    fi = torch.finfo(dtype)
+    least, bits = fi.smallest_normal * fi.eps, 10 if dtype == torch.float16 else 7
+    n = np.random.default_rng(1).integers(-2 ** bits + 1, 2 ** bits, (M, K))
+    c.x = torch.from_numpy(n * least).to(dtype).cuda()
+    assert np.array_equal(f64(c.x), n * least)
+    c.up_s *= np.float32(2.0 ** -bits / least)
+    Y = c.check()
+    assert float(Y.float().abs().mean()) > 1e-3
 
 
 def test_moe_large_products():
