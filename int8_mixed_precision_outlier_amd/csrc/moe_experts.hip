@@ -499,12 +499,12 @@ struct Wide {
 };
 
 template <int TY, int T>
-__device__ __forceinline__ void up_wide(const MoeCall& c, int e, int j0, int n,
+__device__ __forceinline__ void up_wide(const MoeCall& c, int group, int e, int j0, int n,
                                         const uint16_t* list, uint8_t* smem) {
   const int lane = threadIdx.x & 63, q4 = lane >> 4, r16 = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   using P = Wide<TY, T, 1>;
-  const int f = blockIdx.x * P::WAVES + w, nf = c.I / 16, fc = min(f, nf - 1);
+  const int f = group * P::WAVES + w, nf = c.I / 16, fc = min(f, nf - 1);
   P p;
   p.K = c.K;
   p.KB = (c.K + kFp8Block - 1) / kFp8Block;
@@ -530,12 +530,12 @@ __device__ __forceinline__ void up_wide(const MoeCall& c, int e, int j0, int n,
 }
 
 template <int T>
-__device__ __forceinline__ void down_wide(const MoeCall& c, int e, int j0, int n,
+__device__ __forceinline__ void down_wide(const MoeCall& c, int group, int e, int j0, int n,
                                           const uint16_t* list, uint8_t* smem) {
   const int lane = threadIdx.x & 63, q4 = lane >> 4, r16 = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   using P = Wide<kBf16, T, 2>;
-  const int rb0 = (blockIdx.x * P::WAVES + w) * 2, nrb = c.K / 16;
+  const int rb0 = (group * P::WAVES + w) * 2, nrb = c.K / 16;
   P p;
   p.K = c.I;
   p.KB = (c.I + kFp8Block - 1) / kFp8Block;
@@ -571,21 +571,25 @@ template <int PLANES>
 constexpr int kWideLds = 2 * Wide<kF16, 4, PLANES>::STAGE;
 
 // UP: the first product, else the second.  Up to 64 of an expert's tokens per
-// pass over its weights.
+// pass over its weights.  `groups` workgroups make an expert's features; they run
+// on one XCD, whose L2 then holds the expert's tokens for all of them.
 template <int TY, bool UP>
-__global__ __launch_bounds__(512, 4) void k_moe_wide(MoeCall c) {
+__global__ __launch_bounds__(512, 4) void k_moe_wide(MoeCall c, int groups) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int counts[8];
-  constexpr int TILE = kWideLds<UP ? 1 : 2>;
-  uint16_t* list = reinterpret_cast<uint16_t*>(smem + TILE);
+  // The counts lie where the tiles will be: the tiles and a list of the most pairs
+  // are 80 KB, two workgroups fill a CU's LDS to the byte (with 32 bytes more one
+  // fits: the second product of 1024x4096, 128 experts, 8 places took 394 us, not 306).
+  int* counts = reinterpret_cast<int*>(smem);
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + kWideLds<UP ? 1 : 2>);
+  const int at = xcd_remap(blockIdx.x, gridDim.x), group = at % groups;
   int n;
-  const int e = expert_of_slot<512>(c, blockIdx.y, list, counts, n);
+  const int e = expert_of_slot<512>(c, at / groups, list, counts, n);
   if (e < 0) return;
   auto pass = [&](auto t, int j0) {
     if constexpr (UP)
-      up_wide<TY, t()>(c, e, j0, n, list, smem);
+      up_wide<TY, t()>(c, group, e, j0, n, list, smem);
     else
-      down_wide<t()>(c, e, j0, n, list, smem);
+      down_wide<t()>(c, group, e, j0, n, list, smem);
   };
   for (int j0 = 0; j0 < n; j0 += 64) {
     const int blocks = (n - j0 + 15) / 16;
@@ -863,8 +867,8 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeCall c) {
 // Launches with more than the 64 KB of dynamic LDS that need no leave: asked
 // for once per device the kernels run on.
 template <typename Kernel>
-hipError_t launch_big(Kernel kern, std::atomic<uint64_t>& asked, dim3 grid, int threads, size_t lds,
-                      const MoeCall& c, hipStream_t st) {
+hipError_t launch_wide(Kernel kern, std::atomic<uint64_t>& asked, int groups, int slots, size_t lds,
+                       const MoeCall& c, hipStream_t st) {
   int dev = 0;
   (void)hipGetDevice(&dev);
   const uint64_t bit = 1ull << (dev & 63);
@@ -874,7 +878,7 @@ hipError_t launch_big(Kernel kern, std::atomic<uint64_t>& asked, dim3 grid, int 
     if (e != hipSuccess) return e;
     asked.fetch_or(bit, std::memory_order_relaxed);
   }
-  kern<<<grid, threads, lds, st>>>(c);
+  kern<<<groups * slots, 512, lds + (size_t)c.M * c.top_k * 2, st>>>(c, groups);
   return hipGetLastError();
 }
 
@@ -897,14 +901,13 @@ hipError_t split_down(const MoeCall& c, int slots, hipStream_t st) {
 template <int TY>
 hipError_t wide_up(const MoeCall& c, int slots, hipStream_t st) {
   static std::atomic<uint64_t> asked;
-  return launch_big(k_moe_wide<TY, true>, asked, dim3((c.I / 16 + 7) / 8, slots), 512,
-                    kWideLds<1> + (size_t)c.M * c.top_k * 2, c, st);
+  return launch_wide(k_moe_wide<TY, true>, asked, (c.I / 16 + 7) / 8, slots, kWideLds<1>, c, st);
 }
 
 inline hipError_t wide_down(const MoeCall& c, int slots, hipStream_t st) {
   static std::atomic<uint64_t> asked;
-  return launch_big(k_moe_wide<kBf16, false>, asked, dim3((c.K / 16 + 15) / 16, slots), 512,
-                    kWideLds<2> + (size_t)c.M * c.top_k * 2, c, st);
+  return launch_wide(k_moe_wide<kBf16, false>, asked, (c.K / 16 + 15) / 16, slots, kWideLds<2>, c,
+                     st);
 }
 
 // Whether each pair goes alone: one token, or so few pairs that they seldom
