@@ -130,6 +130,17 @@ __device__ __forceinline__ void barrier_vm() {
   asm volatile("" ::: "memory");
 }
 
+// Waits until at most VM of this wavefront's vector-memory operations are
+// outstanding; no memory access moves across.
+template <int VM>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(VM < 64, "waitcnt field");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(VM));
+  asm volatile("" ::: "memory");
+}
+
 // Direct global->LDS load of 16 bytes per lane through a buffer descriptor:
 // lane i's bytes (from voff + soff, soff wave-uniform) land at lds + 16 * i
 // (lds must be wave-uniform).  A descriptor with a record count of 0 makes

@@ -85,6 +85,19 @@ __device__ __forceinline__ v4f mfma16_e4m3(v8i a, v8i b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, v4f{}, 0, 0, 0, 0, 0, 0);
 }
 
+// 16x16x32 matrix instruction on fp16 or bf16 operands with fp32 accumulation
+// (lane convention as mfma16_f16).
+template <int T>
+__device__ __forceinline__ v4f mfma32(v4i a, v4i b, v4f c) {
+  if constexpr (T == kF16) {
+    return mfma16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c);
+  } else {
+    typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a),
+                                                   __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+  }
+}
+
 // ---- packed layout of an e4m3 weight: 16-row x 128-column blocks of 2 KB,
 // row-block major, columns zero-padded to a multiple of 128.  Inside a block
 // the eight 16-byte column chunks are stored chunk-major, so each half block

@@ -28,17 +28,6 @@
 
 namespace i8mm {
 
-// Waits until at most VM of this wavefront's vector-memory operations are
-// outstanding; no memory access moves across.
-template <int VM>
-__device__ __forceinline__ void wait_vm() {
-  static_assert(VM < 64, "waitcnt field");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(VM));
-  asm volatile("" ::: "memory");
-}
-
 // LDS: two stages of a K block per wavefront, each T x 16 rows of 128 bytes
 // and their scales (64 tokens per DMA); at the end the partial sums.
 template <int R, int T, int KS>

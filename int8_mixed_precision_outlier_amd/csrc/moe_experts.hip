@@ -28,19 +28,6 @@ namespace {
 // for the offsets inside a block.
 constexpr uint32_t kNoRow = 0xfffff000u;
 
-typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-
-// 16x16x32 matrix instruction on fp16 or bf16 operands (lane convention as
-// mfma16_f16).
-template <int TY>
-__device__ __forceinline__ v4f mfma32(v4i a, v4i b, v4f c) {
-  if constexpr (TY == kF16)
-    return mfma16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a),
-                                                   __builtin_bit_cast(v8b, b), c, 0, 0, 0);
-}
-
 // Two e4m3 numbers (the low or high half of a dword) as fp16 or bf16, exactly.
 template <int TY, bool HIGH>
 __device__ __forceinline__ int widen2(int w) {

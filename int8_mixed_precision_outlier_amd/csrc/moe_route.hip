@@ -19,8 +19,6 @@ namespace i8mm {
 
 namespace {
 
-typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-
 // ---- few tokens: one wavefront per token and expert, its lanes share the columns
 
 // The sum of x * w in 64 bits over 8 columns from `first` on and again after each
@@ -64,30 +62,13 @@ __global__ __launch_bounds__(256) void k_moe_logits(const uint16_t* __restrict__
 // sums are added at the end, in the wavefronts' order.  Every instruction starts
 // from zero, so that its sum of 32 products is rounded only inside it; a second
 // one on the operands' magnitudes gives the bound.
-template <int TY>
-__device__ __forceinline__ v4f mfma32(v4i a, v4i b, v4f c) {
-  if constexpr (TY == kF16)
-    return mfma16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a),
-                                                   __builtin_bit_cast(v8b, b), c, 0, 0, 0);
-}
-
 // What a sum of 32 products may be off, relative to the sum of their magnitudes:
 // each of its additions within 2^-23 of what it has by then, and a quarter more
 // for the bound's own rounding (at most K / 32 additions of 2^-23).
 constexpr float kLost = 40.0f * 0x1p-23f;
-// Logits closer than this are always compared in 64 bits: subnormal numbers may
-// have been taken for zeros.
+// Logits closer than this are always compared in 64 bits: the bound does not hold
+// for sums below fp32's normal numbers.
 constexpr float kTiny = 0x1p-100f;
-
-template <int VM>
-__device__ __forceinline__ void wait_vm() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(VM));
-  asm volatile("" ::: "memory");
-}
 
 template <int EW, int KS>
 struct Tile {

@@ -30,7 +30,14 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-template <int T, bool QUANT, int NT, int C>
+// 16 bytes; STREAM: nontemporally.
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+  const v4i* from = reinterpret_cast<const v4i*>(p);
+  return __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load(from) : *from);
+}
+
+template <int T, bool QUANT, bool STREAM, int NT, int C>
 __global__ __launch_bounds__(NT) void k_sandwich_norm(SandwichCall c, int m0) {
   __shared__ float part[2][NT / 64];
   const int t = threadIdx.x;
@@ -45,7 +52,7 @@ __global__ __launch_bounds__(NT) void k_sandwich_norm(SandwichCall c, int m0) {
   for (int i = 0; i < C; ++i) {
     const int k = (i * NT + t) * 8;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (k < K) v = *reinterpret_cast<const uint4*>(c.X + base + k);
+    if (k < K) v = load16<STREAM>(c.X + base + k);
     unpack8<T>(v, h[i]);
   }
   // the other operands' loads do not wait for the sum where registers hold them
@@ -57,7 +64,7 @@ __global__ __launch_bounds__(NT) void k_sandwich_norm(SandwichCall c, int m0) {
     rr = p = make_uint4(0, 0, 0, 0);
     g = make_uint4(one, one, one, one);
     if (k < K) {
-      rr = *reinterpret_cast<const uint4*>(c.R + base + k);
+      rr = load16<STREAM>(c.R + base + k);
       p = *reinterpret_cast<const uint4*>(c.post + k);
       if (gate) g = *reinterpret_cast<const uint4*>(gate + k);
     }
@@ -125,9 +132,17 @@ __global__ __launch_bounds__(NT) void k_sandwich_norm(SandwichCall c, int m0) {
 // Rows per launch: a launch holds fewer than 2^32 threads.
 constexpr int kRowsPerLaunch = 1 << 20;
 
+// Rows that the last-level cache (256 MB) cannot hold with what is written are
+// read past it (4096x12288 quantized 79.5 -> 70.9 us = 5.0 TB/s, 16 bits 86.0 ->
+// 73.7); smaller ones may be there still from their making (calls in turn on
+// 220 MB, 2048x5120: 16.9 us, past it 20.1).
 template <int T, int NT, int C>
 hipError_t run(const SandwichCall& c, hipStream_t st) {
-  auto kern = c.Y ? k_sandwich_norm<T, false, NT, C> : k_sandwich_norm<T, true, NT, C>;
+  const bool stream = (int64_t)c.M * c.K * 6 > (256ll << 20);
+  auto kern = c.Y ? (stream ? k_sandwich_norm<T, false, true, NT, C>
+                            : k_sandwich_norm<T, false, false, NT, C>)
+                  : (stream ? k_sandwich_norm<T, true, true, NT, C>
+                            : k_sandwich_norm<T, true, false, NT, C>);
   for (int64_t m0 = 0; m0 < c.M; m0 += kRowsPerLaunch)
     kern<<<(int)(c.M - m0 < kRowsPerLaunch ? c.M - m0 : kRowsPerLaunch), NT, 0, st>>>(c, (int)m0);
   return hipGetLastError();
@@ -136,9 +151,9 @@ hipError_t run(const SandwichCall& c, hipStream_t st) {
 // Threads and chunks of 8 columns per thread that hold a row of K <= 65536.  Two
 // or three chunks per thread let more rows share a CU than one (us, calls in a
 // graph, bf16: 4096x4096, 512 x 1 and 256 x 2: 23.3 and 22.1; 2048x5120, 640 x 1,
-// 512 x 2, 384 x 2, 256 x 3: 20.4, 18.7, 18.1, 16.8; 4096x12288, 768 x 2, 512 x 3,
-// 384 x 4, 256 x 6: 81.2, 77.4, 83.4, 82.7 = 4.6 TB/s); a few rows wait for one
-// row's latency (1x5120, 384 x 2 and 256 x 3: 6.0 and 6.6).
+// 512 x 2, 384 x 2, 256 x 3: 20.4, 18.7, 18.1, 16.8; 4096x12288 through the cache,
+// 768 x 2, 512 x 3, 384 x 4, 256 x 6: 81.2, 77.4, 83.4, 82.7); a few rows wait for
+// one row's latency (1x5120, 384 x 2 and 256 x 3: 6.0 and 6.6).
 template <int T>
 hipError_t shape(const SandwichCall& c, hipStream_t st) {
   const int chunks = (c.K + 7) / 8;

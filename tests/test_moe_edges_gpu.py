@@ -386,6 +386,25 @@ def test_route_most_tokens(M, K, E, k):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("quantize", [True, False])
+@pytest.mark.parametrize("M,K", [(4096, 12288), (12000, 4096), (24000, 2048), (90000, 512), (3000, 16384), (1500, 32784),
+                                 (1000, 65536)])
+def test_sandwich_norm_past_the_cache(M, K, quantize):
+    """Rows of more bytes than the last-level cache holds: what a call on a few of
+    them gives, bit for bit."""
+    x, r = rows(64, K, torch.bfloat16, 1), rows(64, K, torch.bfloat16, 2)
+    post, pre, gate = (rows(1, K, torch.bfloat16, s, outliers=0)[0] for s in (3, 4, 5))
+    n = -(-M // 64)
+    call = lambda a, b: i8.fp8_sandwich_norm(a, b, post, pre, gate=gate, quantize=quantize)  # noqa: E731
+    want = call(x, r)
+    got = call(x.repeat(n, 1)[:M], r.repeat(n, 1)[:M])
+    for a, b, tokens_last in zip(got, want, (False, quantize, False)):
+        b = b.repeat(1, n)[:, :M] if tokens_last else b.view(torch.uint8).repeat(n, 1)[:M]
+        assert torch.equal(a if tokens_last else a.view(torch.uint8), b)
+    del got
+    torch.cuda.empty_cache()
+
+
 def test_sandwich_norm_at_the_size_limit():
     """2^31 elements, and more rows than one launch takes: the last rows."""
     for M, K, G in ((32768, 65536, 2), ((1 << 21) + 6, 16, (1 << 20) + 3)):
