@@ -95,11 +95,12 @@ def _at(t):
 
 def _quantized(out, M, K, device, like=None):
     """The (e4m3 [M, K], scales [ceil(K/128), M]) a quantizer writes: `out`, or
-    new (empty_like, where a tensor of that shape is at hand, is the faster call)."""
+    new (empty_like, where a tensor of that shape is at hand, and sizes that are no
+    tuple are the faster calls)."""
     if out is None:
         return (torch.empty((M, K), dtype=_E4M3, device=device) if like is None
                 else torch.empty_like(like, dtype=_E4M3),
-                torch.empty((_blocks(K), M), dtype=torch.float32, device=device))
+                torch.empty(_blocks(K), M, dtype=torch.float32, device=device))
     q, s = out
     return (_tensor(q, "out[0]", (_E4M3,), (M, K), device),
             _tensor(s, "out[1]", (torch.float32,), (_blocks(K), M), device))
