@@ -518,7 +518,8 @@ size_t moe_route_workspace_size(int64_t M, int64_t K, int64_t E, int64_t top_k);
  *   X        in  [M][K], W in [E][K], 16-bit of one type.
  *   experts  out [M][top_k] int32, weights out [M][top_k] fp32.
  * The order is that of logits summed in 64 bits.  For more than 2^25 products
- * (M * K * E) the weights come from logits within 2^-18 sum |x w| of those.  A NaN logit ranks with -inf and
+ * (M * K * E) the weights come from logits within 2^-18 sum |x w| of those.  A
+ * NaN logit ranks with -inf and
  * makes all of its token's weights NaN; the experts are distinct and in range
  * whatever the logits.
  *   workspace    device, 256-byte aligned, moe_route_workspace_size bytes, no

@@ -203,8 +203,9 @@ def fp8_sandwich_norm(X: torch.Tensor, residual: torch.Tensor, post_weight: torc
     _tensor(pre_weight, "pre_weight", one, (K,), dev)
     gates = 0
     if gate is not None:
-        gates = 1 if gate.dim() == 1 else gate.shape[0]
-        _tensor(gate, "gate", one, (K,) if gate.dim() == 1 else (None, K), dev)
+        row = isinstance(gate, torch.Tensor) and gate.dim() == 1
+        _tensor(gate, "gate", one, (K,) if row else (None, K), dev)
+        gates = 1 if row else gate.shape[0]
         if gates == 0 or M % gates:
             raise ValueError(f"gate has {gates} rows, which do not divide {M} tokens")
     H = residual_out

@@ -12,9 +12,10 @@ from __future__ import annotations
 
 import torch
 
-from . import (FP8_BLOCK, MOE_MAX_EXPERTS, MOE_MAX_PAIRS, MOE_MAX_TOP_K, build_outlier_cache, fp8_matmul, fp8_moe, fp8_pack_experts,
-               fp8_pack_weight, fp8_quantize, fp8_quantize_weight, fp8_rms_norm, fp8_sandwich_norm,
-               mixed_matmul, mixed_matmul_cached, moe_route, quantize_weight, workspace_size)
+from . import (FP8_BLOCK, MOE_MAX_EXPERTS, MOE_MAX_PAIRS, MOE_MAX_TOP_K, build_outlier_cache,
+               fp8_matmul, fp8_moe, fp8_pack_experts, fp8_pack_weight, fp8_quantize,
+               fp8_quantize_weight, fp8_rms_norm, fp8_sandwich_norm, mixed_matmul,
+               mixed_matmul_cached, moe_route, quantize_weight, workspace_size)
 
 _HALVES = (torch.float16, torch.bfloat16)
 

@@ -21,7 +21,8 @@ from . import _check, load
 from .fp8 import (_E4M3, _HALVES, _TYPES, _at, _blocks, _current, _elsewhere, _stream_of, _tensor,
                   fp8_kpad)
 
-__all__ = ["MOE_MAX_EXPERTS", "MOE_MAX_TOP_K", "MOE_MAX_PAIRS", "moe_route", "fp8_moe", "fp8_pack_experts", "fp8_quantize_experts"]
+__all__ = ["MOE_MAX_EXPERTS", "MOE_MAX_TOP_K", "MOE_MAX_PAIRS", "moe_route", "fp8_moe",
+           "fp8_pack_experts", "fp8_quantize_experts"]
 
 MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 1024, 32
 MOE_MAX_PAIRS = 8192  # tokens * top_k of one fp8_moe call
@@ -90,6 +91,8 @@ def moe_route(X: torch.Tensor, W: torch.Tensor, top_k: int, normalize: bool = Tr
     dev = X.device
     _tensor(W, "W", (X.dtype,), (None, K), dev)
     E = W.shape[0]
+    if not 0 <= top_k <= MOE_MAX_TOP_K:  # not a size to allocate
+        raise ValueError(f"top_k must be 1 to {MOE_MAX_TOP_K}, got {top_k}")
     if out is None:
         # sizes by themselves and empty_like: 0.4 us less each than a tuple of sizes
         experts = torch.empty(M, top_k, dtype=torch.int32, device=dev)

@@ -129,3 +129,13 @@ def test_refusals():
     with pytest.raises(i8.Int8mmError):
         moe(X=many, experts=torch.zeros((len(many), 2), dtype=torch.int32, device="cuda"),
             weights=torch.zeros((len(many), 2), device="cuda"))
+
+
+def test_refuses_what_is_no_gate_and_no_size():
+    x = rows(4, 272, torch.float16, 1)
+    for gate, err in ((2.0, TypeError), (x[0, 0], ValueError), (x[0].cpu(), TypeError)):
+        with pytest.raises(err):
+            i8.fp8_sandwich_norm(x, x, x[0], x[1], gate=gate)
+    for top_k in (-1, i8.MOE_MAX_TOP_K + 1, 1 << 40):
+        with pytest.raises(ValueError):
+            i8.moe_route(x, x, top_k)
