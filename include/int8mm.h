@@ -540,7 +540,10 @@ size_t fp8_moe_workspace_size(int64_t M, int64_t K, int64_t I, int64_t E, int64_
  *     a[p] = silu(X[m] . G_e^T) * (X[m] . U_e^T)    for the pairs p = (m, j), e = experts[p]
  *     Y[m] = sum over j of weights[p] * (a[p] . D_e^T)
  * with fp32 sums, the pairs of a token added in the order of j, rounded once (a
- * between the products is held to 2^-17; silu as in fp8_silu_mul).
+ * between the products is held to 2^-17; silu as in fp8_silu_mul).  A block's
+ * scale does not wait for its sum where that could pass fp32's range: results are
+ * infinite or NaN only where the products' sums, a or the pairs' sum themselves
+ * are out of it.
  * Each expert that some token has is read once for (up to 64 of) its tokens,
  * so the call is made for few tokens per expert.
  *   X              in  [M][K], 16-bit, Y out [M][K] of the same type.

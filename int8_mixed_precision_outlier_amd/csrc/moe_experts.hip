@@ -7,8 +7,8 @@
 // chosen expert is read once for all its tokens, and the activations stay in 16
 // bits: quantizing them would not shorten the stream.  The e4m3 numbers become
 // fp16 or bf16 in registers (exactly) and meet the tokens in 16x16x32 matrix
-// instructions; the sum of a 128-column block is scaled once in fp32.  The
-// gated product between the two kernels keeps 16 bits of mantissa as a sum of
+// instructions; the sum of a 128-column block is scaled once in fp32 (see
+// split_scale).  The gated product between the two kernels keeps 16 bits of mantissa as a sum of
 // two bf16 numbers, which feed two matrix instructions each: one bf16 number
 // would add as much error as the result's own rounding, and an fp16 one could
 // overflow.
@@ -28,22 +28,46 @@ namespace {
 // for the offsets inside a block.
 constexpr uint32_t kNoRow = 0xfffff000u;
 
-// Two e4m3 numbers (the low or high half of a dword) as fp16 or bf16, exactly.
+// A block's scale s = power * rest, exactly, the same for the whole wavefront.
+// Left operands of fp32's range times numbers of up to 448, 128 times, can pass it
+// where s brings the sum back, so the conversions of the block's numbers take its
+// power of two with them (they read no more than the exponent), and what multiplies
+// the sum is 1 to 2 in magnitude: the sum passes the range only where its scaled
+// value nearly does.  The power stays within 2^-100 .. 2^100, so that the numbers
+// times it are normal bf16 ones; a scale further out (or zero, subnormal, infinite,
+// NaN) leaves the rest to `rest`.  fp16 operands' sums cannot pass fp32's range,
+// and fp16 could not hold the scaled numbers.
+struct Scale {
+  float power, rest;
+};
+template <int TY>
+__device__ __forceinline__ Scale split_scale(float s) {
+  if constexpr (TY == kF16) return {1.0f, s};
+  // scalar instructions: the median of three is a vector one, and takes registers
+  const int low = max((int)(__builtin_bit_cast(uint32_t, s) >> 23 & 255), 27);
+  const int e = min(__builtin_amdgcn_readfirstlane(low), 227);
+  const float rest = s * __builtin_bit_cast(float, (254 - e) << 23);
+  return {__builtin_bit_cast(float, e << 23),
+          __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, rest)))};
+}
+
+// Two e4m3 numbers (the low or high half of a dword) as fp16, or times a power of
+// two as bf16, exactly.
 template <int TY, bool HIGH>
-__device__ __forceinline__ int widen2(int w) {
+__device__ __forceinline__ int widen2(int w, float power) {
   if constexpr (TY == kF16)
     return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH));
   else
-    return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
+    return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, HIGH));
 }
 
 // A lane's 16 e4m3 numbers of a half block as two matrix operands.
 template <int TY>
-__device__ __forceinline__ void widen16(const v4i& w, v4i (&o)[2]) {
+__device__ __forceinline__ void widen16(const v4i& w, float power, v4i (&o)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    o[i] = v4i{widen2<TY, false>(w[2 * i]), widen2<TY, true>(w[2 * i]),
-               widen2<TY, false>(w[2 * i + 1]), widen2<TY, true>(w[2 * i + 1])};
+    o[i] = v4i{widen2<TY, false>(w[2 * i], power), widen2<TY, true>(w[2 * i], power),
+               widen2<TY, false>(w[2 * i + 1], power), widen2<TY, true>(w[2 * i + 1], power)};
 }
 
 // The expert of slot s: the experts in turn, or, where there are fewer pairs
@@ -150,16 +174,19 @@ struct Product {
 
   __device__ __forceinline__ void compute(const Stage& s, v4f (&acc)[NB][T]) const {
     v4f sum[NB][T];
+    Scale sc[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b) {
+      sc[b] = split_scale<TY>(s.s[b]);
 #pragma unroll
       for (int t = 0; t < T; ++t) sum[b][t] = v4f{};
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         v4i w[2];
-        widen16<TY>(s.w[b][h], w);
+        widen16<TY>(s.w[b][h], sc[b].power, w);
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -172,7 +199,7 @@ struct Product {
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[b][t][e] = fmaf(sum[b][t][e], s.s[b], acc[b][t][e]);
+        for (int e = 0; e < 4; ++e) acc[b][t][e] = fmaf(sum[b][t][e], sc[b].rest, acc[b][t][e]);
   }
 
   __device__ __forceinline__ void run(int w, v4f (&acc)[NB][T]) const {
@@ -429,10 +456,13 @@ struct Wide {
     };
     auto compute = [&](const Weights& o, int stage) {
       v4i w[2][NB][2];
+      Scale sc[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) sc[b] = split_scale<TY>(o.s[b]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) widen16<TY>(o.w[b][h], w[h][b]);
+        for (int b = 0; b < NB; ++b) widen16<TY>(o.w[b][h], sc[b].power, w[h][b]);
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         const uint8_t* row = smem + stage * STAGE + (t * 16 + r16) * ROW;
@@ -453,7 +483,7 @@ struct Wide {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[b][t][e] = fmaf(sum[b][e], o.s[b], acc[b][t][e]);
+          for (int e = 0; e < 4; ++e) acc[b][t][e] = fmaf(sum[b][e], sc[b].rest, acc[b][t][e]);
         // one block of tokens' reads at a time: more would not fit the registers
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -595,7 +625,8 @@ __global__ __launch_bounds__(512, 4) void k_moe_wide(MoeCall c, int groups) {
 //
 // With far fewer pairs than experts an expert has hardly ever two tokens, so each
 // pair goes alone, without matrix instructions: a lane multiplies its 16 numbers
-// of a row by the pair's activations (fp32, in LDS, read by 16 lanes at once).
+// of a row, times their scale's power of two, by the pair's activations (fp32, in
+// LDS, read by 16 lanes at once).
 // That needs one accumulator a row block and no operand registers, so that many
 // wavefronts fit a CU with CB blocks of weights on their way each, refilled as
 // they are used; these calls wait for latency (1x4096 of 128 experts, 8 places of
@@ -654,6 +685,11 @@ __device__ __forceinline__ void vector_product(const uint8_t* W, uint32_t w_byte
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
       float sum[NB][2] = {};
+      Scale sc[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        sc[b] = split_scale<kBf16>(__builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, now[b]), c)));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const v4f* from = reinterpret_cast<const v4f*>(at + c * 128 + h * 64 + q4 * 16);
@@ -663,8 +699,9 @@ __device__ __forceinline__ void vector_product(const uint8_t* W, uint32_t w_byte
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             typedef float v2f __attribute__((ext_vector_type(2)));
-            const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[c][b][h][d], false);
-            const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[c][b][h][d], true);
+            const float p = sc[b].power;
+            const v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[c][b][h][d], p, false);
+            const v2f hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[c][b][h][d], p, true);
             sum[b][0] = fmaf(lo[0], v[0], sum[b][0]);
             sum[b][1] = fmaf(lo[1], v[1], sum[b][1]);
             sum[b][0] = fmaf(hi[0], v[2], sum[b][0]);
@@ -678,11 +715,7 @@ __device__ __forceinline__ void vector_product(const uint8_t* W, uint32_t w_byte
       load_w(kb + CB + c, w[c]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const float sc = __builtin_bit_cast(
-            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, now[b]), c));
-        acc[b] = fmaf(sum[b][0] + sum[b][1], sc, acc[b]);
-      }
+      for (int b = 0; b < NB; ++b) acc[b] = fmaf(sum[b][0] + sum[b][1], sc[b].rest, acc[b]);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before it is written again
   }

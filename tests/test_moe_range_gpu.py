@@ -1,0 +1,84 @@
+"""The experts' products at the ends of fp32's range, where the sum of a block's
+products passes it and the block's scale brings it back; tolerances as derived in
+test_moe_gpu.py."""
+import numpy as np
+import pytest
+import torch
+
+import int8_mixed_precision_outlier_amd as i8
+from oracle import fp8_block as F
+from oracle import moe as O
+from tests.test_moe_gpu import KERNELS, TYPES, Case, f64, near
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M,K,I,E,k", KERNELS)
+@pytest.mark.parametrize("power", [100, 118])
+def test_large_tokens_small_scales(M, K, I, E, k, power):
+    """bf16 tokens near the type's end: a block's numbers times them add up to more
+    than fp32 holds, times the block's scale they do not."""
+    c = Case(M, K, I, E, k, torch.bfloat16, seed=23)
+    c.x = (c.x.float().clamp(-500, 500) * 2.0 ** power).bfloat16()
+    assert torch.isfinite(c.x).all()
+    c.up_s *= np.float32(2.0 ** -power)
+    Y = c.check()
+    assert float(Y.float().abs().mean()) > 1e-3
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,K,I,E,k", KERNELS)
+def test_large_gated_products_small_scales(M, K, I, E, k, dtype):
+    """The same in the second product: gated products of about 2^120.  Of 400 tokens
+    one has a gated product of 2^128.15 by the formula, which fp32 does not hold:
+    tokens whose own gated products pass fp32's range are not compared."""
+    c = Case(M, K, I, E, k, dtype, seed=25)
+    c.up_s *= np.float32(2.0 ** 58)
+    c.down_s *= np.float32(2.0 ** -116)
+    largest = np.zeros(M)
+    for e in range(E):
+        m, _ = np.nonzero(c.experts == e)
+        if len(m):
+            a = F.silu_mul64(f64(c.x)[m] @ O.weight64(c.up[e], c.up_s[e]).T)
+            np.maximum.at(largest, m, np.abs(a).max(1))
+    held = largest < np.finfo(np.float32).max
+    assert held.sum() >= 0.99 * M
+    want, tol = c.oracle()
+    assert np.all(np.isfinite(want)) and np.abs(want).mean() > 1e-3
+    near(i8.fp8_moe(*c.gpu())[torch.from_numpy(held).cuda()], want[held], tol[held], dtype, (M, K, I, E, k))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,K,I,E,k", KERNELS)
+def test_scales_of_every_kind(M, K, I, E, k, dtype):
+    """Scales that are negative, zero, subnormal, and past 2^100 with numbers that
+    bring them back, next to ordinary ones."""
+    c = Case(M, K, I, E, k, dtype, seed=27)
+    c.up_s[:, 0] *= np.float32(-1)
+    c.up_s[:, -1, -1] = 0.0
+    c.down_s[:, 0, 0] = np.float32(2.0 ** -140)
+    c.down_s[:, -1] *= np.float32(-1.75)
+    c.check()
+    c = Case(M, K, I, E, k, dtype, seed=29)
+    # the least number, 2^-9, in a block of scale 2^104: 2^95 times tokens of 2^-95
+    # and below (fp16 tokens cannot be that small: the scale of their products is)
+    if dtype == torch.bfloat16:
+        c.x = (c.x.float() * 2.0 ** -100).bfloat16()
+        c.up &= 0x81
+        c.up_s = (c.up_s * np.float32(2.0 ** 113)).astype(np.float32)
+        assert c.up_s.max() > 2.0 ** 101 and np.abs(f64(c.x)).max() < 2.0 ** -90
+        c.check()
+        assert float(i8.fp8_moe(*c.gpu()).float().abs().max()) > 0
+
+
+@pytest.mark.parametrize("M,K,I,E,k", KERNELS)
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_scales_that_are_no_numbers(M, K, I, E, k, bad):
+    """An infinite or NaN scale makes its expert's tokens infinite or NaN, and no others."""
+    c = Case(M, K, I, E, k, torch.bfloat16, seed=31)
+    e = int(c.experts[0, 0])
+    hit = torch.from_numpy((c.experts == e).any(1)).cuda()
+    want = i8.fp8_moe(*c.gpu())
+    c.down_s[e] = bad
+    Y = i8.fp8_moe(*c.gpu())
+    assert not torch.isfinite(Y[hit]).any() and torch.equal(Y[~hit], want[~hit])
