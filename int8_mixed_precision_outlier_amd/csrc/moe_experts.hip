@@ -247,9 +247,12 @@ __device__ __forceinline__ void store_gated(const v4f& g, const v4f& u, uint8_t*
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float a = silu_mul(g[i], u[i]);
+    // a finite one past the largest bf16 number is that number and a rest; an
+    // infinity leaves none (its difference would be NaN)
+    constexpr float kLargest = 3.4028235e38f, kLargestBf16 = 0x1.fep127f;
     hi[i] = (float)(__bf16)a;
-    // an infinity leaves no rest (and its difference would be NaN)
-    lo[i] = fabsf(hi[i]) <= 3.4028235e38f ? a - hi[i] : 0.0f;
+    if (fabsf(a) > kLargestBf16 && fabsf(a) <= kLargest) hi[i] = copysignf(kLargestBf16, a);
+    lo[i] = fabsf(hi[i]) <= kLargest ? a - hi[i] : 0.0f;
   }
   *reinterpret_cast<uint2*>(at) =
       make_uint2(pack16x2<kBf16>(hi[0], hi[1]), pack16x2<kBf16>(hi[2], hi[3]));

@@ -82,3 +82,19 @@ def test_scales_that_are_no_numbers(M, K, I, E, k, bad):
     c.down_s[e] = bad
     Y = i8.fp8_moe(*c.gpu())
     assert not torch.isfinite(Y[hit]).any() and torch.equal(Y[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,K,I,E,k", KERNELS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_gated_products_between_the_largest_bf16_and_fp32_numbers(M, K, I, E, k, dtype, sign):
+    """2^128 (1 - 2^-12)^2: the nearest bf16 number would be infinite."""
+    c = Case(M, K, I, E, k, dtype, seed=33)
+    c.x[:] = 0
+    c.x[:, 0] = 1
+    c.up[:] = 0
+    c.up[:, :I, 0], c.up[:, I:, 0] = 0x38, 0x38 if sign > 0 else 0xb8  # 1 and 1 or -1
+    c.up_s[:] = np.float32(2.0 ** 64 * (1 - 2.0 ** -12))
+    c.down_s *= np.float32(2.0 ** -128)
+    Y = c.check()
+    assert float(Y.float().abs().mean()) > 1e-3
