@@ -43,10 +43,11 @@ __device__ __forceinline__ double dot64(const uint16_t* x, const uint16_t* w, in
 
 template <int TY>
 __global__ __launch_bounds__(256) void k_moe_logits(const uint16_t* __restrict__ X,
-                                                    const uint16_t* __restrict__ W, int M, int K,
-                                                    int E, double* __restrict__ L) {
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= (int64_t)M * E) return;
+                                                    const uint16_t* __restrict__ W, int64_t first,
+                                                    int64_t dots, int K, int E,
+                                                    double* __restrict__ L) {
+  const int64_t i = first + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (i >= dots) return;
   const int lane = threadIdx.x & 63;
   const double v = dot64<TY>(X + i / E * K, W + i % E * K, K, lane * 8, 512);
   if (lane == 0) L[i] = v;
@@ -345,7 +346,13 @@ hipError_t route(const RouteCall& call, hipStream_t st) {
   const int64_t dots = (int64_t)c.M * c.E;
   if (!route_by_tiles(c.M, c.K, c.E)) {
     c.bound = nullptr;
-    k_moe_logits<TY><<<(unsigned)((dots + 3) / 4), 256, 0, st>>>(c.X, c.W, c.M, c.K, c.E, c.logits);
+    // a launch holds fewer than 2^32 threads; rows without columns can be 2^28 sums
+    constexpr int64_t kPerLaunch = 1 << 24;
+    for (int64_t i = 0; i < dots; i += kPerLaunch) {
+      const int64_t n = dots - i < kPerLaunch ? dots - i : kPerLaunch;
+      k_moe_logits<TY><<<(unsigned)((n + 3) / 4), 256, 0, st>>>(c.X, c.W, i, dots, c.K, c.E,
+                                                                c.logits);
+    }
   } else {
     auto go = [&](auto kern, int ew, size_t lds, std::atomic<uint64_t>& asked) {
       int dev = 0;
