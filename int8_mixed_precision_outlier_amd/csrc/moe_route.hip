@@ -277,8 +277,10 @@ __global__ __launch_bounds__(256) void k_moe_topk(RouteCall c) {
       const double value = key_value(mine);
       const double next = __shfl_down(value, 1, kWave);
       // neighbours whose order is open; not (value - next > off): also where one
-      // of them is no number
-      const uint64_t gaps = __ballot(lane + 1 < count && !(value - next > off));
+      // of them is no number.  A single expert has none, but its sum may have
+      // passed fp32's range and would make its weight NaN.
+      const bool alone = count == 1 && lane == 0 && !(off < __builtin_inf());
+      const uint64_t gaps = __ballot((lane + 1 < count && !(value - next > off)) || alone);
       close = gaps != 0;
       // who has such a neighbour is summed again; the others stay further than
       // `off` from them and from each other
