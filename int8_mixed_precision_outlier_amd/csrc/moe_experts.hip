@@ -499,6 +499,8 @@ struct Wide {
     Weights a, b;
     constexpr int WOPS = 2 * NB;  // vector loads of a block's weights
     load_x(0, 0);
+    // the waits count the loads behind the tile's, so none may be moved in front of it
+    __builtin_amdgcn_sched_barrier(0);
     load_w(0, a);
     load_w(min(1, KB - 1), b);
     barrier_vm<2 * WOPS>();  // the first tile is there
