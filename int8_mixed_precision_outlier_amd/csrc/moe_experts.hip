@@ -871,7 +871,7 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeCall c) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int p = m * c.top_k + min(j0 + j, c.top_k - 1);
-      made[j] = j0 + j < c.top_k && (unsigned)c.experts[p] < (unsigned)c.E;
+      made[j] = j0 + j < c.top_k && (unsigned)c.experts[p] < (unsigned)c.E && c.I > 0;
       const v4f* from = reinterpret_cast<const v4f*>(c.part + (size_t)p * c.K + k);
       u[j] = from[0];
       v[j] = from[1];
@@ -949,7 +949,7 @@ bool few_pairs(const MoeCall& c) {
 template <int TY>
 hipError_t run_few(const MoeCall& c, hipStream_t st) {
   const int P = c.M * c.top_k;
-  if (c.I > 0) k_moe_up_few<TY><<<dim3(c.I / 16, P), kFewUpWaves * 64, 0, st>>>(c);
+  k_moe_up_few<TY><<<dim3(c.I / 16, P), kFewUpWaves * 64, 0, st>>>(c);
   const int parts = P < kFewDownWaves ? kFewDownWaves / P : 1;
   k_moe_down_few<TY><<<c.K / 16, kFewDownWaves * 64, 0, st>>>(c, parts);
   return hipGetLastError();
@@ -989,10 +989,12 @@ hipError_t second_product(const MoeCall& c, int slots, hipStream_t st) {
 template <int TY>
 hipError_t run(const MoeCall& c, hipStream_t st) {
   const int P = c.M * c.top_k, slots = P < c.E ? P : c.E;
-  if (few_pairs(c)) return run_few<TY>(c, st);
-  hipError_t e = c.I > 0 ? first_product<TY>(c, slots, st) : hipSuccess;
-  if (e == hipSuccess) e = second_product(c, slots, st);
-  if (e != hipSuccess) return e;
+  if (c.I > 0) {  // else nothing is made, and the sums over the pairs are zeros
+    if (few_pairs(c)) return run_few<TY>(c, st);
+    hipError_t e = first_product<TY>(c, slots, st);
+    if (e == hipSuccess) e = second_product(c, slots, st);
+    if (e != hipSuccess) return e;
+  }
   k_moe_join<TY><<<(unsigned)(((int64_t)c.M * (c.K / 8) + 255) / 256), 256, 0, st>>>(c);
   return hipGetLastError();
 }

@@ -98,3 +98,19 @@ def test_gated_products_between_the_largest_bf16_and_fp32_numbers(M, K, I, E, k,
     c.down_s *= np.float32(2.0 ** -128)
     Y = c.check()
     assert float(Y.float().abs().mean()) > 1e-3
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,k", [(0, 2), (1, 2), (1, 32), (3, 2), (30, 9), (4000, 2)])
+def test_no_features_between_the_products(M, k, dtype):
+    """I = 0 writes zeros whatever the pairs' weights and experts are."""
+    E, K = 64, 400
+    e8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)  # noqa: E731
+    f = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    x = torch.full((M, K), float("nan"), dtype=dtype, device="cuda")
+    experts = torch.arange(M * k, dtype=torch.int32, device="cuda").remainder(E + 2).sub(1).view(M, k)
+    out = torch.full_like(x, 7)
+    for weight in (1.0, float("nan"), float("inf")):
+        w = torch.full((M, k), weight, device="cuda")
+        assert i8.fp8_moe(x, experts, w, e8(E, 0, 512), f(E, 0, 4), e8(E, K, 0), f(E, 4, 0), out=out.fill_(7)) is out
+        assert bool((out == 0).all())
