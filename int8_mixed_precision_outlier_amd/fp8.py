@@ -206,7 +206,7 @@ def fp8_sandwich_norm(X: torch.Tensor, residual: torch.Tensor, post_weight: torc
         row = isinstance(gate, torch.Tensor) and gate.dim() == 1
         _tensor(gate, "gate", one, (K,) if row else (None, K), dev)
         gates = 1 if row else gate.shape[0]
-        if gates == 0 or M % gates:
+        if M % gates if gates else M:  # no rows: one for each of no tokens
             raise ValueError(f"gate has {gates} rows, which do not divide {M} tokens")
     H = residual_out
     if H is None:
