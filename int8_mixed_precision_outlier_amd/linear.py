@@ -309,7 +309,7 @@ class Fp8MoE(torch.nn.Module):
         most = min(router.shape[0], MOE_MAX_TOP_K)
         if not 1 <= top_k <= most:
             raise ValueError(f"top_k must be 1 to {most}, got {top_k}")
-        self.register_buffer("router", router.detach().clone())
+        self.register_buffer("router", router.detach().clone(memory_format=torch.contiguous_format))
         for name, t in (("gate_up", gate_up), ("gate_up_scale", gate_up_scale), ("down", down),
                         ("down_scale", down_scale)):
             self.register_buffer(name, t)
