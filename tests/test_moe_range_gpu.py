@@ -114,3 +114,16 @@ def test_no_features_between_the_products(M, k, dtype):
         w = torch.full((M, k), weight, device="cuda")
         assert i8.fp8_moe(x, experts, w, e8(E, 0, 512), f(E, 0, 4), e8(E, K, 0), f(E, 4, 0), out=out.fill_(7)) is out
         assert bool((out == 0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,K,I,E,k", KERNELS)
+@pytest.mark.parametrize("power", [40, 56, 60])
+def test_small_gated_products_large_scales(M, K, I, E, k, dtype, power):
+    """Gated products of about 2^(-2 power), whose second bf16 number is below the
+    type's normal ones, and a second matrix that brings them back."""
+    c = Case(M, K, I, E, k, dtype, seed=35)
+    c.up_s *= np.float32(2.0 ** -power)
+    c.down_s *= np.float32(2.0 ** (2 * power))
+    Y = c.check()
+    assert float(Y.float().abs().mean()) > 1e-3
