@@ -390,8 +390,11 @@ __global__ __launch_bounds__(KS * 64) void k_moe_down(MoeCall c) {
 // A workgroup's eight wavefronts take two blocks of 16 weight rows each, over all
 // columns, and share the tokens' tile of a 128-column block in LDS, which comes by
 // DMA a block ahead (two blocks ahead it took as long: 512x4096 of 128 experts
-// 541 and 546 us).  The weights go straight to the wavefront that uses them, up to
-// two blocks ahead.
+// 541 and 546 us).  The weights go straight to the wavefront that uses them,
+// requested two blocks ahead.  The loop goes by two blocks and may end after the
+// first, so the compiled first step waits for all but 0 to 5 of the loads on their
+// way, the next block's weights and tile among them, in front of its products; only
+// the second step's run under the stream.  The figures here are with those waits.
 // A tile row is 256 bytes per number of an operand column, its 16-byte chunks
 // swapped by the row's low four bits: a read of 16 bytes serves 16 lanes at once,
 // eight of one chunk and eight of the next one, and they meet all 64 banks (by
@@ -635,8 +638,10 @@ __global__ __launch_bounds__(512, 4) void k_moe_wide(MoeCall c, int groups) {
 // That needs one accumulator a row block and no operand registers, so that many
 // wavefronts fit a CU with CB blocks of weights on their way each, refilled as
 // they are used; these calls wait for latency (1x4096 of 128 experts, 8 places of
-// 1408: 29.5 us in a graph, 17 + 10 in the two kernels = 5.2 TB/s; CB = 4 and 6,
-// without the order of the reads below, 32).
+// 1408: 30 us in a graph, 18 + 10.5 in the two kernels = 5.1 TB/s; CB = 4 and 6,
+// without the order of the reads below, 32).  The compiler orders the first CB
+// blocks' loads as it likes and has a round's first use wait for all that are on
+// their way; the figures are with that wait.
 
 // The sums over columns [kb0, kb1) * 128 of NB row blocks; lane l has that of row
 // l % 16 in every of its four quarters.  x.load(kb) starts the loads of the
